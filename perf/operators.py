@@ -320,8 +320,8 @@ def _own_router_grad(s):
         s["adot"] = torch.empty(c["T"] * c["k"], device=DEV)
         s["dlogits"] = torch.empty(c["T"], c["E"], device=DEV)
     lrm.lrm_gate_dots(s["problem"], s["sel_pair"], s["cmp_off"], s["dphi"], s["Phic"], s["adot"], s["ws"])
-    lrm.lrm_route_backward(s["router"], s["logits"], s["topk_idx"], s["topk_w"], s["lse"],
-                           s["counts"], s["adot"], s["dlogits"])
+    lrm.lrm_route_backward(s["router"], s["logits"], s["topk_idx"], s["topk_w"], s["counts"],
+                           s["adot"], s["dlogits"])
     return {"adot": s["adot"], "dlogits": s["dlogits"]}
 
 
