@@ -1,8 +1,14 @@
 // Host side of the C ABI declared in include/lrm.h: argument validation, workspace layout and
 // kernel launches.  No allocation, no synchronisation (except lrm_read_device_error).
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "lrm_forward.hpp"
 #include "lrm_internal.hpp"
 
 using lrm::WsLayout;
@@ -11,6 +17,8 @@ namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+static_assert(sizeof(lrm_router) == 24 && sizeof(lrm_tensor) == 32,
+              "lrm_router and lrm_tensor layouts are part of the ABI");
 static_assert(sizeof(lrm_admission) == 248 && offsetof(lrm_admission, mem_budget) == 208,
               "lrm_admission layout is part of the ABI");
 
@@ -48,6 +56,78 @@ lrm_problem fc1_problem(const lrm_problem& p) {
   q.h = 2 * p.d;
   q.d = p.h;
   return q;
+}
+
+lrm_status check_router(const lrm_router* r) {
+  if (!r) return LRM_ERR_INVALID_ARGUMENT;
+  if (r->T <= 0 || r->E <= 0 || r->k <= 0 || r->k > r->E) return LRM_ERR_INVALID_ARGUMENT;
+  if (r->gate != LRM_GATE_TOPK && r->gate != LRM_GATE_ALL) return LRM_ERR_INVALID_ARGUMENT;
+  if (!(r->balance_coef >= 0.0f) || r->balance_coef == INFINITY) return LRM_ERR_INVALID_ARGUMENT;
+  if (r->dtype != LRM_F32 && r->dtype != LRM_BF16) return LRM_ERR_UNSUPPORTED;
+  if (r->E > 4096 || (int64_t)r->T * r->k > INT32_MAX) return LRM_ERR_UNSUPPORTED;
+  return LRM_OK;
+}
+
+lrm_status check_forward_ws(const lrm_problem* p, const void* ws, size_t ws_bytes) {
+  if (!ws) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(ws)) return LRM_ERR_UNSUPPORTED;
+  return ws_bytes < lrm::forward_ws_bytes(*p) ? LRM_ERR_WORKSPACE_TOO_SMALL : LRM_OK;
+}
+
+int64_t element_bytes(int32_t dtype) { return dtype == LRM_BF16 ? 2 : 4; }
+
+// Largest operand the forward products address with 32-bit byte offsets.
+constexpr int64_t kMaxOperand = (int64_t)1 << 31;
+
+// The list's entries are well formed; with `write`, also that no element is written by one entry
+// and read or written by another, nor by an entry whose dst overlaps its src without being it.
+lrm_status check_tensors(const lrm_tensor* list, int32_t n, bool write) {
+  if (n < 0 || (n > 0 && !list)) return LRM_ERR_INVALID_ARGUMENT;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const lrm_tensor& t = list[i];
+    if (t.count < 0 || t.reserved != 0) return LRM_ERR_INVALID_ARGUMENT;
+    if (t.dtype != LRM_F32 && t.dtype != LRM_BF16) return LRM_ERR_UNSUPPORTED;
+    if (t.count >= ((int64_t)1 << 46) || (total += t.count) >= ((int64_t)1 << 46))
+      return LRM_ERR_UNSUPPORTED;
+    if (t.count == 0) continue;
+    const uintptr_t e = (uintptr_t)element_bytes(t.dtype) - 1;
+    if (!t.src || (write && !t.dst)) return LRM_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)t.src & e) || (write && ((uintptr_t)t.dst & e))) return LRM_ERR_UNSUPPORTED;
+  }
+  if (!write) return LRM_OK;
+  struct Range {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  std::vector<Range> ranges;
+  try {
+    ranges.reserve(2 * (size_t)n);
+  } catch (const std::bad_alloc&) {
+    return LRM_ERR_UNSUPPORTED;
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    const lrm_tensor& t = list[i];
+    if (t.count == 0) continue;
+    const uintptr_t bytes = (uintptr_t)(t.count * element_bytes(t.dtype));
+    ranges.push_back({(uintptr_t)t.dst, (uintptr_t)t.dst + bytes, true});
+    if (t.src != t.dst) ranges.push_back({(uintptr_t)t.src, (uintptr_t)t.src + bytes, false});
+  }
+  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  // in order of their starts: a range overlaps an earlier one if it starts before that one's end
+  uintptr_t end = 0, written_end = 0;
+  for (const Range& r : ranges) {
+    if (r.lo < written_end || (r.written && r.lo < end)) return LRM_ERR_INVALID_ARGUMENT;
+    end = std::max(end, r.hi);
+    if (r.written) written_end = std::max(written_end, r.hi);
+  }
+  return LRM_OK;
+}
+
+lrm_status check_grad_ws(int32_t n, const void* ws, size_t ws_bytes) {
+  if (!ws) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(ws)) return LRM_ERR_UNSUPPORTED;
+  return ws_bytes < lrm::grad_ws_bytes(n) ? LRM_ERR_WORKSPACE_TOO_SMALL : LRM_OK;
 }
 
 }  // namespace
@@ -298,6 +378,103 @@ lrm_status lrm_scatter_tokens(const lrm_problem* problem, const int32_t* sel_pai
   LRM_TRY(check_ws(problem, ws, ws_bytes, &wl));
   return from_hip(lrm::launch_scatter_tokens(*problem, sel_pair, cmp_off, dX, dx, (char*)ws, wl,
                                              stream));
+}
+
+size_t lrm_router_workspace_bytes(const lrm_router* router) {
+  return check_router(router) == LRM_OK ? lrm::route_ws(router->E).total : 0;
+}
+
+lrm_status lrm_route(const lrm_router* router, const void* logits, const uint8_t* mask,
+                     int32_t* topk_idx, float* topk_w, float* lse, int32_t* counts, float* prob,
+                     float* loss, void* ws, size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_router(router));
+  if (!logits || !topk_idx || !topk_w || !lse || !counts || !prob || !loss || !ws)
+    return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(logits) || !aligned16(ws)) return LRM_ERR_UNSUPPORTED;
+  if (ws_bytes < lrm::route_ws(router->E).total) return LRM_ERR_WORKSPACE_TOO_SMALL;
+  return from_hip(lrm::launch_route(*router, logits, mask, topk_idx, topk_w, lse, counts, prob, loss,
+                                    (char*)ws, stream));
+}
+
+lrm_status lrm_route_backward(const lrm_router* router, const void* logits,
+                              const int32_t* topk_idx, const float* topk_w, const int32_t* counts,
+                              const float* adot, float* dlogits, hipStream_t stream) {
+  LRM_TRY(check_router(router));
+  if (!logits || !topk_idx || !topk_w || !counts || !dlogits) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(logits) || !aligned16(dlogits)) return LRM_ERR_UNSUPPORTED;
+  return from_hip(lrm::launch_route_backward(*router, logits, topk_idx, topk_w, counts, adot,
+                                             dlogits, stream));
+}
+
+lrm_status lrm_gate_dots(const lrm_problem* problem, const int32_t* sel_pair,
+                         const int32_t* cmp_off, const float* dphi, const void* Phic, float* adot,
+                         void* ws, size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_problem(problem));
+  if (!sel_pair || !cmp_off || !dphi || !Phic || !adot) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(dphi) || !aligned16(Phic)) return LRM_ERR_UNSUPPORTED;
+  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
+  return from_hip(lrm::launch_gate_dots(*problem, sel_pair, cmp_off, dphi, Phic, adot, (char*)ws,
+                                        stream));
+}
+
+size_t lrm_forward_workspace_bytes(const lrm_problem* problem) {
+  return check_problem(problem) == LRM_OK ? lrm::forward_ws_bytes(*problem) : 0;
+}
+
+lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row_pair,
+                                  const int32_t* fwd_off, const void* x, const void* W1, void* ac,
+                                  void* phi, void* ws, size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_problem(problem));
+  if (!row_pair || !fwd_off || !x || !W1 || !phi) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(W1) || !aligned16(ac) || !aligned16(phi)) return LRM_ERR_UNSUPPORTED;
+  const int64_t row = problem->h * element_bytes(problem->dtype);
+  if (problem->T * row > kMaxOperand || 2 * problem->d * row > kMaxOperand) return LRM_ERR_UNSUPPORTED;
+  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
+  return from_hip(lrm::launch_fc1_swiglu(*problem, row_pair, fwd_off, x, W1, ac, phi, (char*)ws,
+                                         stream));
+}
+
+lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
+                           const void* W, void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_problem(problem));
+  if (!fwd_off || !phi || !W || !y) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(phi) || !aligned16(W) || !aligned16(y)) return LRM_ERR_UNSUPPORTED;
+  if ((int64_t)problem->h * problem->d * element_bytes(problem->dtype) > kMaxOperand)
+    return LRM_ERR_UNSUPPORTED;
+  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
+  return from_hip(lrm::launch_fc2(*problem, fwd_off, phi, W, y, stream));
+}
+
+lrm_status lrm_combine_tokens(const lrm_problem* problem, const int32_t* row_pair,
+                              const int32_t* fwd_off, const float* topk_w, const void* y,
+                              const void* residual, void* out, void* ws, size_t ws_bytes,
+                              hipStream_t stream) {
+  LRM_TRY(check_problem(problem));
+  if (!row_pair || !fwd_off || !topk_w || !y || !out) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(out)) return LRM_ERR_UNSUPPORTED;
+  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
+  return from_hip(lrm::launch_combine(*problem, row_pair, fwd_off, topk_w, y, residual, out,
+                                      (char*)ws, stream));
+}
+
+size_t lrm_grad_workspace_bytes(const lrm_tensor* list, int32_t n) {
+  return check_tensors(list, n, false) == LRM_OK ? lrm::grad_ws_bytes(n) : 0;
+}
+
+lrm_status lrm_grad_norm(const lrm_tensor* list, int32_t n, float* norm, void* ws, size_t ws_bytes,
+                         hipStream_t stream) {
+  LRM_TRY(check_tensors(list, n, false));
+  if (!norm) return LRM_ERR_INVALID_ARGUMENT;
+  LRM_TRY(check_grad_ws(n, ws, ws_bytes));
+  return from_hip(lrm::launch_grad_norm(list, n, norm, (char*)ws, stream));
+}
+
+lrm_status lrm_clip_grads(const lrm_tensor* list, int32_t n, float max_norm, float* norm, void* ws,
+                          size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_tensors(list, n, true));
+  if (!norm || !(max_norm > 0.0f) || max_norm == INFINITY) return LRM_ERR_INVALID_ARGUMENT;
+  LRM_TRY(check_grad_ws(n, ws, ws_bytes));
+  return from_hip(lrm::launch_clip(list, n, max_norm, norm, (char*)ws, stream));
 }
 
 lrm_status lrm_read_device_error(void* ws, int32_t* code, int32_t clear, hipStream_t stream) {

@@ -23,10 +23,16 @@ EXPORTS = ("lrm_workspace_bytes", "lrm_plan_quotas", "lrm_admit_quotas", "lrm_sc
            "lrm_select", "lrm_compact", "lrm_grouped_dw", "lrm_grouped_dx", "lrm_grouped_dw_dx",
            "lrm_swiglu_backward", "lrm_gather_tokens", "lrm_grouped_fc1_dw", "lrm_grouped_fc1_dx",
            "lrm_grouped_fc1_dw_dx", "lrm_scatter_tokens", "lrm_read_device_error",
-           "lrm_status_string", "lrm_grouped_dw_dx_noalloc")
+           "lrm_status_string", "lrm_grouped_dw_dx_noalloc", "lrm_router_workspace_bytes",
+           "lrm_route", "lrm_route_backward", "lrm_gate_dots", "lrm_forward_workspace_bytes",
+           "lrm_grouped_fc1_swiglu", "lrm_grouped_fc2", "lrm_combine_tokens",
+           "lrm_grad_workspace_bytes", "lrm_grad_norm", "lrm_clip_grads")
+_SIZES = ("lrm_workspace_bytes", "lrm_router_workspace_bytes", "lrm_forward_workspace_bytes",
+          "lrm_grad_workspace_bytes")
 
 QUOTA_KINDS = {"cap": 0, "proportional": 1, "waterfill": 2}
 CRITERIA = {"lrm": 0, "grad_sq": 1, "grad_abs": 2, "random": 3}
+GATES = {"topk": 0, "all": 1}
 
 
 class Problem(ctypes.Structure):
@@ -36,6 +42,16 @@ class Problem(ctypes.Structure):
 
 class QuotaPolicy(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("full", "rho_num", "rho_den", "cap_abs", "kind")]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "dtype", "gate")] + \
+               [("balance_coef", ctypes.c_float)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 MAX_CANDIDATES = 16
@@ -85,7 +101,6 @@ def load_library(path: Optional[str] = None):
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
     PP, QP = ctypes.POINTER(Problem), ctypes.POINTER(QuotaPolicy)
     lib.lrm_workspace_bytes.argtypes = [PP]
-    lib.lrm_workspace_bytes.restype = sz
     lib.lrm_plan_quotas.argtypes = [PP, QP] + [vp] * 7 + [sz, vp]
     lib.lrm_admit_quotas.argtypes = [PP, ctypes.POINTER(Admission)] + [vp] * 5 + [sz, vp]
     lib.lrm_score.argtypes = [PP] + [vp] * 7 + [sz, vp]
@@ -105,8 +120,22 @@ def load_library(path: Optional[str] = None):
     lib.lrm_grouped_fc1_dw_dx.argtypes = [PP] + [vp] * 7 + [sz, vp]
     lib.lrm_scatter_tokens.argtypes = [PP] + [vp] * 5 + [sz, vp]
     lib.lrm_read_device_error.argtypes = [vp, ctypes.POINTER(i32), i32, vp]
+    RP, TP = ctypes.POINTER(Router), ctypes.POINTER(Tensor)
+    lib.lrm_router_workspace_bytes.argtypes = [RP]
+    lib.lrm_route.argtypes = [RP] + [vp] * 9 + [sz, vp]
+    lib.lrm_route_backward.argtypes = [RP] + [vp] * 7
+    lib.lrm_gate_dots.argtypes = [PP] + [vp] * 6 + [sz, vp]
+    lib.lrm_forward_workspace_bytes.argtypes = [PP]
+    lib.lrm_grouped_fc1_swiglu.argtypes = [PP] + [vp] * 7 + [sz, vp]
+    lib.lrm_grouped_fc2.argtypes = [PP] + [vp] * 5 + [sz, vp]
+    lib.lrm_combine_tokens.argtypes = [PP] + [vp] * 7 + [sz, vp]
+    lib.lrm_grad_workspace_bytes.argtypes = [TP, i32]
+    lib.lrm_grad_norm.argtypes = [TP, i32, vp, vp, sz, vp]
+    lib.lrm_clip_grads.argtypes = [TP, i32, ctypes.c_float, vp, vp, sz, vp]
     for f in EXPORTS:
-        if f not in ("lrm_workspace_bytes", "lrm_status_string"):
+        if f in _SIZES:
+            getattr(lib, f).restype = sz
+        elif f != "lrm_status_string":
             getattr(lib, f).restype = ctypes.c_int
     lib.lrm_status_string.argtypes = [ctypes.c_int]
     lib.lrm_status_string.restype = ctypes.c_char_p
@@ -288,6 +317,189 @@ def lrm_scatter_tokens(problem, sel_pair, cmp_off, dX, dx, ws, stream=None):
     _check(lib, lib.lrm_scatter_tokens(ctypes.byref(problem), _ptr(sel_pair), _ptr(cmp_off),
                                        _ptr(dX), _ptr(dx), *_ws(ws), _stream(stream)),
            "lrm_scatter_tokens")
+
+
+# ---------------------------------------------------------------------------------------------
+# The router, the experts' forward and the clipping of gradients.  A torch tensor's element type,
+# size, layout and device are known here, so these calls check them before they pass the pointer
+# on; a plain address (int) is passed as it is.
+# ---------------------------------------------------------------------------------------------
+
+_ELEM = {LRM_F32: (torch.float32,), LRM_BF16: (torch.bfloat16, torch.int16)}
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
+
+
+def _arg(t, name, types, count, device, exact=False):
+    """The address of tensor ``t`` of at least (or exactly) ``count`` elements, after its checks."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in types:
+        raise LrmError(f"{name}: element type {t.dtype}, expected {types[0]}")
+    n = t.numel()
+    if n < count or (exact and n != count):
+        raise LrmError(f"{name}: {n} elements, expected {'' if exact else 'at least '}{count}")
+    if not t.is_contiguous():
+        raise LrmError(f"{name}: not contiguous")
+    if t.device.type != "cuda" or t.device.index != device:
+        raise LrmError(f"{name}: on {t.device}, the call runs on cuda:{device}")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    return torch.cuda.current_device()
+
+
+def _elem(dtype):
+    if dtype not in _ELEM:
+        raise LrmError(f"unknown element type {dtype}")
+    return _ELEM[dtype]
+
+
+def _space(ws, device):
+    if isinstance(ws, int):
+        raise LrmError("ws: a tensor is needed, its size is part of the call")
+    n = ws.numel() * ws.element_size()
+    return _arg(ws, "ws", (ws.dtype,), 0, device), n
+
+
+def make_router(T, E, k, dtype="f32", gate="topk", balance_coef=0.0) -> Router:
+    """A router over E experts: ``gate`` "topk" renormalises the k weights, "all" keeps the
+    probabilities over all experts; ``dtype`` is the logits'."""
+    dt = {"f32": LRM_F32, "bf16": LRM_BF16}.get(dtype, dtype)
+    return Router(T, E, k, dt, GATES[gate] if isinstance(gate, str) else int(gate), balance_coef)
+
+
+def lrm_router_workspace_bytes(router: Router) -> int:
+    return int(load_library().lrm_router_workspace_bytes(ctypes.byref(router)))
+
+
+def lrm_forward_workspace_bytes(problem: Problem) -> int:
+    return int(load_library().lrm_forward_workspace_bytes(ctypes.byref(problem)))
+
+
+def lrm_route(router, logits, mask, topk_idx, topk_w, lse, counts, prob, loss, ws, stream=None):
+    lib = load_library()
+    r, d = router, _device()
+    _check(lib, lib.lrm_route(ctypes.byref(r), _arg(logits, "logits", _elem(r.dtype), r.T * r.E, d, True),
+                              _arg(mask, "mask", _U8, r.T, d, True),
+                              _arg(topk_idx, "topk_idx", _I32, r.T * r.k, d),
+                              _arg(topk_w, "topk_w", _F32, r.T * r.k, d),
+                              _arg(lse, "lse", _F32, r.T, d), _arg(counts, "counts", _I32, r.E, d),
+                              _arg(prob, "prob", _F32, r.E, d), _arg(loss, "loss", _F32, 1, d),
+                              *_space(ws, d), _stream(stream)), "lrm_route")
+
+
+def lrm_route_backward(router, logits, topk_idx, topk_w, counts, adot, dlogits, stream=None):
+    lib = load_library()
+    r, d = router, _device()
+    _check(lib, lib.lrm_route_backward(
+        ctypes.byref(r), _arg(logits, "logits", _elem(r.dtype), r.T * r.E, d, True),
+        _arg(topk_idx, "topk_idx", _I32, r.T * r.k, d), _arg(topk_w, "topk_w", _F32, r.T * r.k, d),
+        _arg(counts, "counts", _I32, r.E, d),
+        _arg(adot, "adot", _F32, r.T * r.k, d), _arg(dlogits, "dlogits", _F32, r.T * r.E, d),
+        _stream(stream)), "lrm_route_backward")
+
+
+def lrm_gate_dots(problem, sel_pair, cmp_off, dphi, Phic, adot, ws, stream=None):
+    lib = load_library()
+    p, d = problem, _device()
+    _check(lib, lib.lrm_gate_dots(
+        ctypes.byref(p), _arg(sel_pair, "sel_pair", _I32, p.K_cap, d),
+        _arg(cmp_off, "cmp_off", _I32, p.E_loc + 1, d), _arg(dphi, "dphi", _F32, p.K_cap * p.d, d),
+        _arg(Phic, "Phic", _elem(p.dtype), p.K_cap * p.d, d), _arg(adot, "adot", _F32, p.T * p.k, d),
+        *_space(ws, d), _stream(stream)), "lrm_gate_dots")
+
+
+def lrm_grouped_fc1_swiglu(problem, row_pair, fwd_off, x, W1, ac, phi, ws, stream=None):
+    """``ac`` None: the saved FC1 output is not kept (serving)."""
+    lib = load_library()
+    p, d = problem, _device()
+    el = _elem(p.dtype)
+    _check(lib, lib.lrm_grouped_fc1_swiglu(
+        ctypes.byref(p), _arg(row_pair, "row_pair", _I32, p.L_cap, d),
+        _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d), _arg(x, "x", el, p.T * p.h, d),
+        _arg(W1, "W1", el, p.E_loc * 2 * p.d * p.h, d), _arg(ac, "ac", el, p.L_cap * 2 * p.d, d),
+        _arg(phi, "phi", el, p.L_cap * p.d, d), *_space(ws, d), _stream(stream)),
+        "lrm_grouped_fc1_swiglu")
+
+
+def lrm_grouped_fc2(problem, fwd_off, phi, W, y, ws, stream=None):
+    lib = load_library()
+    p, d = problem, _device()
+    el = _elem(p.dtype)
+    _check(lib, lib.lrm_grouped_fc2(
+        ctypes.byref(p), _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d),
+        _arg(phi, "phi", el, p.L_cap * p.d, d), _arg(W, "W", el, p.E_loc * p.h * p.d, d),
+        _arg(y, "y", el, p.L_cap * p.h, d), *_space(ws, d), _stream(stream)), "lrm_grouped_fc2")
+
+
+def lrm_combine_tokens(problem, row_pair, fwd_off, topk_w, y, residual, out, ws, stream=None):
+    """``residual`` None: the experts' output alone; ``out`` may be ``residual``."""
+    lib = load_library()
+    p, d = problem, _device()
+    el = _elem(p.dtype)
+    _check(lib, lib.lrm_combine_tokens(
+        ctypes.byref(p), _arg(row_pair, "row_pair", _I32, p.L_cap, d),
+        _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d), _arg(topk_w, "topk_w", _F32, p.T * p.k, d),
+        _arg(y, "y", el, p.L_cap * p.h, d), _arg(residual, "residual", el, p.T * p.h, d),
+        _arg(out, "out", el, p.T * p.h, d), *_space(ws, d), _stream(stream)), "lrm_combine_tokens")
+
+
+class TensorList:
+    """The (src, dst) tensors of lrm_grad_norm / lrm_clip_grads as the library's host array, made
+    once and used for every step; it keeps the tensors alive."""
+
+    def __init__(self, src, dst):
+        self.src, self.dst = list(src), list(src if dst is None else dst)
+        if len(self.src) != len(self.dst):
+            raise LrmError(f"{len(self.src)} sources, {len(self.dst)} destinations")
+        self.n = len(self.src)
+        self.device = None
+        self.array = (Tensor * max(1, self.n))()
+        kinds = {torch.float32: LRM_F32, torch.bfloat16: LRM_BF16}
+        for i, (a, b) in enumerate(zip(self.src, self.dst)):
+            if a.dtype not in kinds or b.dtype != a.dtype:
+                raise LrmError(f"tensor {i}: element types {a.dtype}, {b.dtype}: float32 or bfloat16, "
+                               "the same for both")
+            if a.device.type != "cuda":
+                raise LrmError(f"tensor {i}: on {a.device}")
+            if self.device is None:
+                self.device = a.device.index
+            n = a.numel()
+            self.array[i] = Tensor(_arg(a, f"tensor {i}", (a.dtype,), n, self.device),
+                                   _arg(b, f"destination {i}", (a.dtype,), n, self.device, True), n,
+                                   kinds[a.dtype], 0)
+
+
+def make_tensor_list(src, dst=None) -> TensorList:
+    """float32 or bfloat16 tensors (contiguous, on one device) and where their clipped values go;
+    ``dst`` None: in place."""
+    return TensorList(src, dst)
+
+
+def lrm_grad_workspace_bytes(tensors: TensorList) -> int:
+    return int(load_library().lrm_grad_workspace_bytes(tensors.array, tensors.n))
+
+
+def _on_device(tensors):
+    d = _device()
+    if tensors.device is not None and tensors.device != d:
+        raise LrmError(f"tensors: on cuda:{tensors.device}, the call runs on cuda:{d}")
+    return d
+
+
+def lrm_grad_norm(tensors, norm, ws, stream=None):
+    lib = load_library()
+    d = _on_device(tensors)
+    _check(lib, lib.lrm_grad_norm(tensors.array, tensors.n, _arg(norm, "norm", _F32, 1, d),
+                                  *_space(ws, d), _stream(stream)), "lrm_grad_norm")
+
+
+def lrm_clip_grads(tensors, max_norm, norm, ws, stream=None):
+    lib = load_library()
+    d = _on_device(tensors)
+    _check(lib, lib.lrm_clip_grads(tensors.array, tensors.n, max_norm, _arg(norm, "norm", _F32, 1, d),
+                                   *_space(ws, d), _stream(stream)), "lrm_clip_grads")
 
 
 def lrm_read_device_error(ws, clear: bool = False, stream=None) -> int:

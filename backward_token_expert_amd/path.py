@@ -7,7 +7,13 @@ stream, runs lrm_score_norms there beside lrm_plan_quotas and lrm_score_combine 
 ``LayerBuffers`` and ``run_layer`` do the same for the rest of the expert backward over the
 retained rows:
 lrm_swiglu_backward -> lrm_gather_tokens -> lrm_grouped_fc1_dw_dx (or the two FC1 calls) ->
-lrm_scatter_tokens.  No step of the path is computed here.
+lrm_scatter_tokens.
+
+The layer's forward and what follows its backward have the same form: ``route`` over
+``RouterBuffers`` (lrm_route), ``run_forward`` over ``ForwardBuffers`` (lrm_plan_quotas ->
+lrm_grouped_fc1_swiglu -> lrm_grouped_fc2 -> lrm_combine_tokens), ``run_router_backward``
+(lrm_gate_dots -> lrm_route_backward) and ``GradientClip`` (lrm_clip_grads over a fixed list of
+gradients).  No step of the path is computed here.
 """
 from __future__ import annotations
 
@@ -139,3 +145,85 @@ def run_layer(problem, ac, x, W1, bufs: DeviceBuffers, lay: LayerBuffers, stream
         lrm.lrm_grouped_fc1_dw(problem, lay.dH, lay.Xc, b.cmp_off, lay.dW1, b.ws, stream)
         lrm.lrm_grouped_fc1_dx(problem, lay.dH, W1, b.cmp_off, lay.dX, b.ws, stream)
     lrm.lrm_scatter_tokens(problem, b.sel_pair, b.cmp_off, lay.dX, lay.dx, b.ws, stream)
+
+
+class RouterBuffers:
+    """Outputs and workspace of one router."""
+
+    def __init__(self, router: lrm.Router, device="cuda"):
+        r = router
+        nws = lrm.lrm_router_workspace_bytes(r)
+        if nws == 0:
+            raise lrm.LrmError("invalid router")
+        i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+        self.topk_idx = torch.zeros(r.T * r.k, **i32)
+        self.topk_w = torch.zeros(r.T * r.k, **f32)
+        self.lse = torch.zeros(r.T, **f32)
+        self.counts = torch.zeros(r.E, **i32)
+        self.prob = torch.zeros(r.E, **f32)
+        self.loss = torch.zeros(1, **f32)
+        self.adot = torch.zeros(r.T * r.k, **f32)
+        self.dlogits = torch.zeros((r.T, r.E), **f32)
+        self.ws = torch.zeros(nws, dtype=torch.uint8, device=device)
+
+
+def route(router, logits, rb: RouterBuffers, mask=None, stream=None):
+    """Enqueue the routing of every token: choices, weights, counts and the balance loss."""
+    lrm.lrm_route(router, logits, mask, rb.topk_idx, rb.topk_w, rb.lse, rb.counts, rb.prob, rb.loss,
+                  rb.ws, stream)
+
+
+class ForwardBuffers:
+    """Outputs of the experts' forward, sized to the problem's capacities.  ``keep_ac`` False (serving):
+    FC1's output is not kept for a backward."""
+
+    def __init__(self, problem: lrm.Problem, device="cuda", keep_ac: bool = True):
+        p = problem
+        st = storage_dtype("bf16" if p.dtype == lrm.LRM_BF16 else "f32")
+        self.ac = torch.zeros((p.L_cap, 2 * p.d), dtype=st, device=device) if keep_ac else None
+        self.phi = torch.zeros((p.L_cap, p.d), dtype=st, device=device)
+        self.y = torch.zeros((p.L_cap, p.h), dtype=st, device=device)
+        self.out = torch.zeros((p.T, p.h), dtype=st, device=device)
+
+
+def run_forward(problem, policy, topk_idx, topk_w, x, W1, W, bufs: DeviceBuffers,
+                fwd: ForwardBuffers, residual=None, stream=None):
+    """Enqueue the experts' forward: the plan (counts, layout and the retention quotas that the
+    backward over the same buffers keeps), FC1 with the activation, FC2, and the weighted sum back
+    to the tokens.  ``fwd.phi`` and ``fwd.ac`` are then what ``run`` and ``run_layer`` take."""
+    b = bufs
+    lrm.lrm_plan_quotas(problem, policy, topk_idx, b.counts, b.fwd_off, b.row_pair, b.quota,
+                        b.cmp_off, b.ws, stream)
+    lrm.lrm_grouped_fc1_swiglu(problem, b.row_pair, b.fwd_off, x, W1, fwd.ac, fwd.phi, b.ws, stream)
+    lrm.lrm_grouped_fc2(problem, b.fwd_off, fwd.phi, W, fwd.y, b.ws, stream)
+    lrm.lrm_combine_tokens(problem, b.row_pair, b.fwd_off, topk_w, fwd.y, residual, fwd.out, b.ws,
+                           stream)
+
+
+def run_router_backward(problem, router, logits, bufs: DeviceBuffers, rb: RouterBuffers,
+                        stream=None):
+    """Enqueue the router's gradient after ``run`` on the same buffers: rb.dlogits holds that of the
+    balance loss and of the retained pairs' gate weights."""
+    lrm.lrm_gate_dots(problem, bufs.sel_pair, bufs.cmp_off, bufs.dphi, bufs.Phic, rb.adot, bufs.ws,
+                      stream)
+    lrm.lrm_route_backward(router, logits, rb.topk_idx, rb.topk_w, rb.counts, rb.adot,
+                           rb.dlogits, stream)
+
+
+class GradientClip:
+    """Clipping of a fixed list of gradients by their global norm, in place unless ``dst`` is given;
+    the list, the norm and the workspace are kept between the steps."""
+
+    def __init__(self, grads, dst=None):
+        self.list = lrm.make_tensor_list(grads, dst)
+        device = self.list.src[0].device if self.list.n else "cuda"
+        nws = lrm.lrm_grad_workspace_bytes(self.list)
+        if nws == 0:
+            raise lrm.LrmError("invalid tensor list")
+        self.norm = torch.zeros(1, dtype=torch.float32, device=device)
+        self.ws = torch.zeros(nws, dtype=torch.uint8, device=device)
+
+    def __call__(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Enqueue the clipping; the norm before it, a device tensor of one element."""
+        lrm.lrm_clip_grads(self.list, max_norm, self.norm, self.ws, stream)
+        return self.norm

@@ -459,6 +459,181 @@ lrm_status lrm_scatter_tokens(const lrm_problem* problem, const int32_t* sel_pai
                               const int32_t* cmp_off, const float* dX, float* dx, void* ws,
                               size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * The layer's forward step and what follows its backward: the router with its balance loss, the
+ * experts' products with the activation and the return to the tokens, the router's gradient, and
+ * the clipping of gradients by their global norm.  One training step of a layer is
+ *   lrm_route -> lrm_plan_quotas -> lrm_grouped_fc1_swiglu -> lrm_grouped_fc2 ->
+ *   lrm_combine_tokens -> (the backward calls above) -> lrm_gate_dots -> lrm_route_backward ->
+ *   lrm_clip_grads;
+ * a serving step is the first five of these with full retention and ac = NULL.
+ * The conventions at the top of this file hold here too, with these additions:
+ *  - Router calls have a problem of their own (lrm_router) and a workspace of
+ *    lrm_router_workspace_bytes; its first word is the error word, which lrm_route sets to the
+ *    bits of that call.
+ *  - lrm_grouped_fc1_swiglu, lrm_grouped_fc2, lrm_combine_tokens and lrm_gate_dots need a workspace of
+ *    lrm_forward_workspace_bytes only (lrm_workspace_bytes of the same problem is always
+ *    enough, so a training step may pass the one it has).  They may overwrite all of those bytes
+ *    but the error word, so not between lrm_score_norms and lrm_score_combine on one workspace.
+ *  - Two calls that may run at the same time need a workspace each.
+ * ------------------------------------------------------------------------------------------------ */
+
+/* Gate weights of the chosen experts. */
+#define LRM_GATE_TOPK 0 /* softmax over the k chosen logits (the weights of a token sum to 1)        */
+#define LRM_GATE_ALL 1  /* the chosen experts' probabilities under the softmax over all E logits      */
+
+typedef struct {
+  int32_t T;            /* tokens                                                                   */
+  int32_t E;            /* global experts, <= 4096                                                  */
+  int32_t k;            /* experts per token, <= E                                                  */
+  int32_t dtype;        /* lrm_dtype of the logits                                                  */
+  int32_t gate;         /* LRM_GATE_*                                                               */
+  float balance_coef;   /* factor of the balance loss, finite and >= 0                              */
+} lrm_router;
+
+/* Bytes of device scratch lrm_route needs (0 if the router is invalid). */
+size_t lrm_router_workspace_bytes(const lrm_router* router);
+
+/*
+ * Top-k routing with the per-expert counts and the balance loss ("Expert Parallel Math Deep",
+ * auxiliary loss: L_aux = coef * E * sum_e f_e P_e).  For every token t with mask[t] != 0:
+ *   lse[t]   = log sum_e exp(l_te),   p_te = exp(l_te - lse[t])
+ *   the k chosen experts in the order (logit descending, expert ascending), and their weights
+ *   under `gate`, each rounded once to float32 from float32 arithmetic;
+ * and over the n valid tokens
+ *   counts[e] = pairs of expert e,  prob[e] = P_e = (1/n) sum_t p_te,
+ *   loss = balance_coef * E * sum_e f_e P_e  with  f_e = counts[e] / (n k)
+ * (P_e's sum over a workgroup's tokens in float32, over workgroups in float64, both in a fixed
+ * order).  A logit of -infinity closes an expert for a token: p_te = 0, and it is chosen (with
+ * weight 0) only where fewer than k logits are finite.  A token whose mask is 0, or whose logits
+ * are all -infinity, is not valid: its topk_idx are -1, its topk_w and lse 0, and it counts
+ * nowhere.  lrm_plan_quotas leaves pairs of expert -1 out (and reports them as
+ * LRM_DEVERR_EXPERT_ID).  With no valid token prob and loss are 0.  A NaN or +infinity sets
+ * LRM_DEVERR_NONFINITE in the workspace's error word; NaN is then ranked as -infinity, the row's
+ * floating results and prob and loss are unspecified, and its indices are still distinct and in
+ * [0, E) unless no logit of the row is left.
+ *  in : logits [T][E] (router->dtype); mask uint8 [T] or NULL (every token valid)
+ *  out: topk_idx int32 [T*k]; topk_w float32 [T*k]; lse float32 [T]; counts int32 [E];
+ *       prob float32 [E]; loss float32 [1]
+ * logits must be 16-byte aligned; rows need not be.
+ */
+lrm_status lrm_route(const lrm_router* router, const void* logits, const uint8_t* mask,
+                     int32_t* topk_idx, float* topk_w, float* lse, int32_t* counts, float* prob,
+                     float* loss, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The router's upstream gradient from what the expert backward already holds.  The layer's output
+ * is sum_j alpha_p W_e phi_r, so dL/dalpha_p = <g_t, W_e phi_r>, and with dphi_i = W_e^T (alpha_p
+ * g_t) of the retained row i (lrm_grouped_dx)
+ *   adot[p] = alpha_p dL/dalpha_p = <dphi[i], Phic[i]>      (float64 sum, one rounding)
+ * The softmax backward needs dL/dalpha_p only in this product, so no division by alpha_p (which
+ * may be 0) takes place.  adot[p] = 0 for every pair that is not retained: a dropped pair adds
+ * nothing to the router's gradient, as it adds nothing to the experts'.
+ *  in : sel_pair int32 [K_cap]; cmp_off (cmp_off[E_loc] = K read); dphi float32 [K_cap][d];
+ *       Phic [K_cap][d]
+ *  out: adot float32 [T*k] (every entry written)
+ * A pair id outside [0, T*k), or two rows naming one pair, sets LRM_DEVERR_INDEX.  dphi and Phic
+ * 16-byte aligned.
+ */
+lrm_status lrm_gate_dots(const lrm_problem* problem, const int32_t* sel_pair,
+                         const int32_t* cmp_off, const float* dphi, const void* Phic, float* adot,
+                         void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gradient of the logits: of the balance loss (factor 1 times lrm_route's loss; the counts are
+ * constants) and, where adot is not NULL, of the gate weights.  With c = balance_coef * E / n, n =
+ * (sum of counts) / k, f_e as in lrm_route, s_j = adot[t*k+j], S = sum_j s_j:
+ *   dlogits[t][e] = c p_te (f_e - sum_e' f_e' p_te')
+ *                   + LRM_GATE_TOPK: s_j - topk_w[t*k+j] S   on the chosen e = topk_idx[t*k+j]
+ *                   + LRM_GATE_ALL:  s_j on the chosen e, and -p_te S on every e
+ * in float32; p_te is formed from the row again, not from lse, which at logits of the type's
+ * lowest value no longer holds the logarithm.  Rows of tokens that lrm_route found not valid (topk_idx[t*k] < 0) are zeros.
+ *  in : logits [T][E]; topk_idx, topk_w, counts as lrm_route wrote them; adot float32 [T*k] or NULL
+ *  out: dlogits float32 [T][E] (every row written)
+ * Needs no workspace.  logits and dlogits must be 16-byte aligned; chosen experts outside [0, E)
+ * are skipped.
+ */
+lrm_status lrm_route_backward(const lrm_router* router, const void* logits,
+                              const int32_t* topk_idx, const float* topk_w, const int32_t* counts,
+                              const float* adot, float* dlogits, hipStream_t stream);
+
+/* Bytes of device scratch the forward calls and lrm_gate_dots need (0 if the problem is invalid). */
+size_t lrm_forward_workspace_bytes(const lrm_problem* problem);
+
+/*
+ * Grouped FC1 with the SwiGLU activation in its epilogue, over every local forward row:  for row r
+ * of local expert i, pair p = row_pair[r], token t = p / k,
+ *   [a; c] = W1_i x_t   (float32 accumulation),   ac[r] = RNE_dtype([a | c]),
+ *   phi[r] = RNE_dtype(SiLU(a) c)  from the unrounded float32 a and c
+ * -- the saved state that lrm_score, lrm_compact and lrm_swiglu_backward read.  The rows of x are
+ * gathered inside the product; no copy of them is made.
+ *  in : row_pair int32 [L_cap], fwd_off int32 [E_loc+1] as lrm_plan_quotas writes them; x [T][h];
+ *       W1 [E_loc][2d][h]
+ *  out: ac [L_cap][2d], or NULL (serving: not kept); phi [L_cap][d]   (first L rows written)
+ * A pair id outside [0, T*k) sets LRM_DEVERR_INDEX and its row reads x as zeros.  x and one
+ * expert's weights must not exceed 2^31 bytes each (LRM_ERR_UNSUPPORTED).  x, W1, ac and phi
+ * 16-byte aligned.
+ */
+lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row_pair,
+                                  const int32_t* fwd_off, const void* x, const void* W1, void* ac,
+                                  void* phi, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Grouped FC2 over every local forward row:  y[r] = RNE_dtype(W_i phi[r])  for the rows r of local
+ * expert i (float32 accumulation).
+ *  in : fwd_off int32 [E_loc+1]; phi [L_cap][d]; W [E_loc][h][d]
+ *  out: y [L_cap][h] (first L rows written)
+ * One expert's weights must not exceed 2^31 bytes (LRM_ERR_UNSUPPORTED).  phi, W and y 16-byte
+ * aligned.
+ */
+lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
+                           const void* W, void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The experts' output rows back to their tokens, weighted, with the residual:
+ *   out[t] = RNE_dtype( residual[t] + sum over slots j = 0..k-1 in order, pair p = t*k + j with a
+ *                       local row r, of topk_w[p] * y[r] )
+ * summed in float32 in that order.  A token without a local row gets residual[t] (zeros without a
+ * residual).
+ *  in : row_pair int32 [L_cap]; fwd_off (fwd_off[E_loc] = L read); topk_w float32 [T*k]; y [L_cap][h];
+ *       residual [T][h] or NULL
+ *  out: out [T][h] (every row written; may be residual itself)
+ * A pair id outside [0, T*k), or two rows naming one pair, sets LRM_DEVERR_INDEX.  y, residual and
+ * out 16-byte aligned.
+ */
+lrm_status lrm_combine_tokens(const lrm_problem* problem, const int32_t* row_pair,
+                              const int32_t* fwd_off, const float* topk_w, const void* y,
+                              const void* residual, void* out, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/*
+ * Global norm of many tensors, and clipping.  The list is host memory, read during the call only.
+ *   norm = sqrt( sum over all tensors and elements of src^2 )   (float64 sums in a fixed order)
+ *   lrm_clip_grads:  dst = RNE_dtype(fl32(src * coef)),  coef = min(1, max_norm / norm) in float32
+ *                    (1 where norm = 0)
+ * dst may be src (in place); a coef of 1 then leaves the tensor unread and unwritten.  A norm that
+ * is NaN or infinite sets LRM_DEVERR_NONFINITE in the workspace's error word (which each of the
+ * two calls sets to its own bits) and no dst is written: the step is the caller's to skip.
+ *  in : list [n] (n >= 0; count >= 0; data aligned to its element); max_norm finite and > 0
+ *  out: norm float32 [1]; dst
+ * No element may be written by one entry and read or written by another: overlapping entries
+ * (other than several that only read, by lrm_grad_norm) return LRM_ERR_INVALID_ARGUMENT, as does
+ * a dst that overlaps its src without being it.  The total number of elements is below 2^46.
+ */
+typedef struct {
+  const void* src;
+  void* dst;            /* lrm_clip_grads only                                                      */
+  int64_t count;        /* elements                                                                 */
+  int32_t dtype;        /* lrm_dtype                                                                */
+  int32_t reserved;     /* 0                                                                        */
+} lrm_tensor;
+
+size_t lrm_grad_workspace_bytes(const lrm_tensor* list, int32_t n);
+lrm_status lrm_grad_norm(const lrm_tensor* list, int32_t n, float* norm, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+lrm_status lrm_clip_grads(const lrm_tensor* list, int32_t n, float max_norm, float* norm, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
 /*
  * Copies the device error word to *code (host).  Synchronises `stream` (tests and diagnostics
  * only, never inside a captured sequence).  If clear != 0 the word is reset to zero afterwards.
