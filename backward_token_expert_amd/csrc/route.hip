@@ -59,12 +59,6 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return v;
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
-}
-
 template <bool kBF16>
 __device__ __forceinline__ float load_logit(const void* row, int e) {
   if (kBF16) return __uint_as_float((uint32_t)((const uint16_t*)row)[e] << 16);
@@ -183,6 +177,257 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void route_any(RouteArgs a) {
   }
 }
 
+// Registers-only routing for k <= KT and E <= LPT * VPL: LPT adjacent lanes share a token, each
+// holding up to VPL logits in 16-byte chunks (chunk i * LPT + sub, so a token's lanes read 16 LPT
+// consecutive bytes).  Each lane keeps its KT largest keys sorted by inserting every key (one
+// maximum and one minimum per place, both single float64 instructions: the insertion costs 2 KT
+// instructions a logit where a compare and four selects would cost 5 KT), then log2(LPT) merges
+// of two sorted lists (maximum of one list against the other reversed, then a bitonic sort) leave
+// the token's list in all its lanes.  Few lanes a token keep the wave's work in the insertions of
+// distinct logits rather than in reductions that every lane repeats.
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// The value of a lane of the other half of each group of 2 * O lanes (all lanes of a half hold the
+// same value when O > 1 and O < 16, so a mirror serves as the exchange).
+template <int O>
+__device__ __forceinline__ int swap_half(int v) {
+  if constexpr (O == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);        // 1 0 3 2
+  else if constexpr (O == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);   // 2 3 0 1
+  else if constexpr (O == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);  // mirror of 8
+  else if constexpr (O == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);  // mirror of 16
+  else return __shfl_xor(v, O, kWave);
+}
+template <int O>
+__device__ __forceinline__ float swap_half(float v) {
+  return __int_as_float(swap_half<O>(__float_as_int(v)));
+}
+template <int O>
+__device__ __forceinline__ double swap_half(double v) {
+  return __hiloint2double(swap_half<O>(__double2hiint(v)), swap_half<O>(__double2loint(v)));
+}
+
+// Sum or maximum over a token's LPT lanes, in all of them.
+template <int LPT, int O = 1>
+__device__ __forceinline__ float token_sum(float v) {
+  if constexpr (O < LPT) return token_sum<LPT, 2 * O>(v + swap_half<O>(v));
+  return v;
+}
+template <int LPT, int O = 1>
+__device__ __forceinline__ float token_max(float v) {
+  if constexpr (O < LPT) return token_max<LPT, 2 * O>(fmaxf(v, swap_half<O>(v)));
+  return v;
+}
+
+template <int KT, int LPT, int O = 1>
+__device__ __forceinline__ void merge_lists(double (&t)[KT]) {
+  if constexpr (O < LPT) {
+    double u[KT];
+#pragma unroll
+    for (int j = 0; j < KT; ++j) u[j] = max64(t[j], swap_half<O>(t[KT - 1 - j]));
+#pragma unroll
+    for (int s = KT / 2; s >= 1; s /= 2)
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        if (!(j & s)) {
+          const double a = u[j], b = u[j + s];
+          u[j] = max64(a, b);
+          u[j + s] = min64(a, b);
+        }
+#pragma unroll
+    for (int j = 0; j < KT; ++j) t[j] = u[j];
+    merge_lists<KT, LPT, 2 * O>(t);
+  }
+}
+
+// exp(v - m) for v <= m by the hardware's power of two: the argument's rounding, (m - v) 2^-24, and
+// the instruction's own are each within what the products around it round.
+__device__ __forceinline__ float exp_below(float v, float m) {
+  return __builtin_amdgcn_exp2f((v - m) * 1.44269504f);
+}
+
+// A lane's logits of one row: VPL values, -infinity past E or where the row is not wanted.  `vec`:
+// rows are multiples of 16 bytes.
+template <bool kBF16, int LPT, int VPL>
+__device__ __forceinline__ void load_row(const char* row, int E, int sub, bool want, bool vec,
+                                         float (&v)[VPL]) {
+  constexpr int CV = kBF16 ? 8 : 4;
+#pragma unroll
+  for (int i = 0; i < VPL / CV; ++i) {
+    const int e0 = (i * LPT + sub) * CV;
+#pragma unroll
+    for (int q = 0; q < CV; ++q) v[i * CV + q] = -INFINITY;
+    if (i * LPT * CV >= E) continue;   // uniform
+    if (vec) {
+      if (want && e0 < E) {
+        const uint4 x = ((const uint4*)row)[i * LPT + sub];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (kBF16) {
+            v[i * CV + 2 * q] = bf16_lo(w[q]);
+            v[i * CV + 2 * q + 1] = bf16_hi(w[q]);
+          } else {
+            v[i * CV + q] = __uint_as_float(w[q]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < CV; ++q)
+        if (want && e0 + q < E) v[i * CV + q] = load_logit<kBF16>(row, e0 + q);
+    }
+  }
+}
+
+struct RouteOut {
+  int32_t* counts;
+  float* prob;
+  float* loss;
+  int32_t* err;
+  float coef;
+};
+
+template <bool kBF16, int LPT, int VPL, int KT, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void route_rows(RouteArgs a, RouteOut o, int vec) {
+  constexpr int CV = kBF16 ? 8 : 4, TPW = kWave / LPT;
+  constexpr int ROWS = LPT <= 16 ? 4 : 1;   // partial sums of a wave: one per 16 lanes, or one
+  constexpr int THREADS = WAVES * kWave;
+  extern __shared__ float shared[];
+  const int E = a.E, lane = lane_id(), w = threadIdx.x / kWave, sub = lane % LPT;
+  float* part = shared;                            // [WAVES * ROWS][E]
+  int* counts = (int*)(shared + WAVES * ROWS * E); // [E]
+  __shared__ int live_sum, bits;
+  for (int e = threadIdx.x; e < E; e += THREADS) counts[e] = 0;
+  if (threadIdx.x == 0) live_sum = bits = 0;
+  __syncthreads();
+  float acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+  int live = 0, bad = 0;
+  const int64_t step = (int64_t)gridDim.x * WAVES * TPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * WAVES + w) * TPW; t0 < a.T; t0 += step) {
+    const int64_t t = t0 + lane / LPT;
+    const bool want = t < a.T && (a.mask == nullptr || a.mask[t]);
+    float v[VPL];
+    load_row<kBF16, LPT, VPL>((const char*)a.logits + (want ? t : 0) * E * (kBF16 ? 2 : 4), E, sub,
+                              want, vec, v);
+    double key[KT];
+#pragma unroll
+    for (int j = 0; j < KT; ++j) key[j] = kNoKey;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i / CV * LPT * CV >= E) continue;   // uniform
+      const int e = (i / CV * LPT + sub) * CV + i % CV;
+      if (bad_logit(v[i])) bad = LRM_DEVERR_NONFINITE;
+      double x = e < E ? route_key(v[i], e) : kNoKey;
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        const double hi = max64(key[j], x);
+        x = min64(key[j], x);
+        key[j] = hi;
+      }
+    }
+    merge_lists<KT, LPT>(key);
+    const float top = key_logit(key[0]);
+    const bool ok = want && top > -INFINITY;
+    const float m = ok ? top : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i / CV * LPT * CV >= E) continue;
+      v[i] = exp_below(v[i], m);
+      sum += v[i];
+    }
+    sum = token_sum<LPT>(sum);
+    const float inv = ok ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i / CV * LPT * CV >= E) continue;
+      acc[i] += v[i] * inv;
+    }
+    float p[KT], chosen = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KT; ++j) {
+      p[j] = exp_below(key_logit(key[j]), m);
+      chosen += j < a.k ? p[j] : 0.0f;
+    }
+    const float scale = a.gate == LRM_GATE_TOPK ? (ok ? 1.0f / chosen : 0.0f) : inv;
+    if (t < a.T) {
+      if (sub == 0) {
+        a.lse[t] = ok ? m + __logf(sum) : 0.0f;
+        live += ok;
+      }
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        if (j % LPT == sub && j < a.k) {
+          const int e = ok ? key_expert(key[j]) : -1;
+          a.topk_idx[t * a.k + j] = e;
+          a.topk_w[t * a.k + j] = p[j] * scale;
+          if (e >= 0) atomicAdd(&counts[e], 1);
+        }
+    }
+  }
+  // over the tokens of a wave: lanes of one sub within 16 lanes by rotations, the rest in LDS
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (i / CV * LPT * CV >= E) continue;
+    float x = acc[i];
+    if constexpr (LPT <= 4) x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xF, 0xF, true));
+    if constexpr (LPT <= 8) x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF, 0xF, true));
+    const int e = (i / CV * LPT + sub) * CV + i % CV;
+    if ((LPT > 16 || lane % 16 < LPT) && e < E) part[(w * ROWS + (ROWS > 1 ? lane / 16 : 0)) * E + e] = x;
+  }
+  live = wave_sum_int(live);
+  const bool any_bad = ballot(bad != 0) != 0;
+  if (lane == 0) {
+    atomicAdd(&live_sum, live);
+    if (any_bad) atomicOr(&bits, LRM_DEVERR_NONFINITE);
+  }
+  __syncthreads();
+  const int n = live_sum;
+  double mine = 0.0;   // of sum_e counts[e] * (sum of p_te), where this workgroup is the only one
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    float x = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < WAVES * ROWS; ++q) x += part[q * E + e];
+    if (gridDim.x > 1) {
+      a.part_prob[(int64_t)blockIdx.x * E + e] = x;
+      a.part_counts[(int64_t)blockIdx.x * E + e] = counts[e];
+    } else {
+      o.counts[e] = counts[e];
+      o.prob[e] = n > 0 ? (float)((double)x / n) : 0.0f;
+      mine += (double)x * counts[e];
+    }
+  }
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      a.part_tokens[2 * blockIdx.x] = n;
+      a.part_tokens[2 * blockIdx.x + 1] = bits;
+    }
+    return;
+  }
+  __shared__ double sums[WAVES];
+  mine = wave_sum(mine);
+  if (lane == 0) sums[w] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double x = 0.0;
+    for (int q = 0; q < WAVES; ++q) x += sums[q];
+    const double nn = n;
+    *o.loss = n > 0 ? (float)((double)o.coef * E * x / (nn * nn * a.k)) : 0.0f;
+    *o.err = bits;
+  }
+}
+
 // Sums the workgroups' partial results: counts, prob, the loss and the error word.  One workgroup
 // of 1024 threads; thread (slice, e) adds every S-th workgroup's row in float64, then slice 0 adds
 // the slices.
@@ -248,55 +493,106 @@ __global__ __launch_bounds__(kFinalThreads) void route_final(const int32_t* __re
   }
 }
 
-// dlogits: one wavefront per token, passes over the row for its maximum, its sums and the output
-// (all but the first from the caches).
-template <bool kBF16>
-__global__ __launch_bounds__(kBlock) void route_backward(const void* __restrict__ logits,
-                                                         const int32_t* __restrict__ topk_idx,
-                                                         const float* __restrict__ topk_w,
-                                                         const int32_t* __restrict__ counts,
-                                                         const float* __restrict__ adot, int T,
-                                                         int E, int k, int gate, float coef,
-                                                         float* __restrict__ dlogits) {
-  const int lane = lane_id();
+// dlogits, with the lanes and registers of route_rows.  The gate's terms on the k chosen experts
+// go through a row of zeros in LDS, where their lanes of the row pick them up; a lane's own
+// register for an expert is not indexable.
+template <bool kBF16, int LPT, int VPL, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void route_backward(const void* __restrict__ logits,
+                                                                const int32_t* __restrict__ topk_idx,
+                                                                const float* __restrict__ topk_w,
+                                                                const int32_t* __restrict__ counts,
+                                                                const float* __restrict__ adot,
+                                                                int T, int E, int k, int gate,
+                                                                float coef, int vec,
+                                                                float* __restrict__ dlogits) {
+  constexpr int CV = kBF16 ? 8 : 4, TPW = kWave / LPT;
+  extern __shared__ float shared[];
+  const int lane = lane_id(), w = threadIdx.x / kWave, sub = lane % LPT;
+  float* extra = shared + (w * TPW + lane / LPT) * E;   // this token's row
   int pairs = 0;
   for (int e = lane; e < E; e += kWave) pairs += counts[e];
   pairs = wave_sum_int(pairs);
   // f_e = counts[e] / (n k) and c = coef E / n with n = pairs / k
   const float f1 = pairs > 0 ? 1.0f / (float)pairs : 0.0f;
   const float c = pairs > 0 ? (float)((double)coef * E * k / pairs) : 0.0f;
-  const int64_t nw = (int64_t)gridDim.x * kWavesPerBlock;
-  for (int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + threadIdx.x / kWave; t < T; t += nw) {
-    const char* row = (const char*)logits + t * E * (kBF16 ? 2 : 4);
-    float* out = dlogits + t * E;
-    if (topk_idx[t * k] < 0) {
-      for (int e = lane; e < E; e += kWave) out[e] = 0.0f;
-      continue;
+  float f[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = (i / CV * LPT + sub) * CV + i % CV;
+    f[i] = e < E ? f1 * counts[e] : 0.0f;
+    if (adot != nullptr && e < E) extra[e] = 0.0f;
+  }
+  const bool vec_out = E % 4 == 0;
+  const int64_t step = (int64_t)gridDim.x * WAVES * TPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * WAVES + w) * TPW; t0 < T; t0 += step) {
+    const int64_t t = t0 + lane / LPT;
+    const bool in = t < T, ok = in && topk_idx[t * k] >= 0;
+    float v[VPL];
+    load_row<kBF16, LPT, VPL>((const char*)logits + (ok ? t : 0) * E * (kBF16 ? 2 : 4), E, sub, ok,
+                              vec, v);
+    float S = 0.0f;
+    if (adot != nullptr) {
+      if (ok)
+        for (int j = sub; j < k; j += LPT) S += adot[t * k + j];
+      S = token_sum<LPT>(S);
+      if (ok)
+        for (int j = sub; j < k; j += LPT) {
+          const int e = topk_idx[t * k + j];
+          const float x = adot[t * k + j] - (gate == LRM_GATE_TOPK ? topk_w[t * k + j] * S : 0.0f);
+          if (e >= 0 && e < E) atomicAdd(&extra[e], x);
+        }
     }
     float m = -INFINITY;
-    for (int e = lane; e < E; e += kWave) m = fmaxf(m, load_logit<kBF16>(row, e));
-    m = wave_max_f32(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i / CV * LPT * CV >= E) continue;
+      m = fmaxf(m, v[i]);
+    }
+    m = token_max<LPT>(m);
+    m = ok ? m : 0.0f;
     float sum = 0.0f, fp = 0.0f;
-    for (int e = lane; e < E; e += kWave) {
-      const float p = expf(load_logit<kBF16>(row, e) - m);
-      sum += p;
-      fp += f1 * counts[e] * p;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i / CV * LPT * CV >= E) continue;
+      v[i] = exp_below(v[i], m);
+      sum += v[i];
+      fp += f[i] * v[i];
     }
-    const float inv = 1.0f / wave_sum_f32(sum);
-    fp = wave_sum_f32(fp) * inv;
-    float S = 0.0f;
-    if (adot != nullptr)
-      for (int j = 0; j < k; ++j) S += adot[t * k + j];
+    const float inv = ok ? 1.0f / token_sum<LPT>(sum) : 0.0f;
+    fp = token_sum<LPT>(fp) * inv;
     const float all = gate == LRM_GATE_ALL ? S : 0.0f;
-    for (int e = lane; e < E; e += kWave) {
-      const float p = expf(load_logit<kBF16>(row, e) - m) * inv;
-      float g = p * (c * (f1 * counts[e] - fp) - all);
-      if (adot != nullptr)
-        for (int j = 0; j < k; ++j)
-          if (topk_idx[t * k + j] == e)
-            g += adot[t * k + j] - (gate == LRM_GATE_TOPK ? topk_w[t * k + j] * S : 0.0f);
-      out[e] = g;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < VPL / 4; ++i) {
+        const int e0 = (i * 4 / CV * LPT + sub) * CV + i * 4 % CV;
+        if (i * 4 / CV * LPT * CV >= E) continue;
+        float g[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          g[q] = v[4 * i + q] * inv * (c * (f[4 * i + q] - fp) - all);
+          if (adot != nullptr && e0 + q < E) g[q] += extra[e0 + q];
+        }
+        float* out = dlogits + t * E + e0;
+        if (vec_out) {
+          if (e0 < E) *(float4*)out = make_float4(g[0], g[1], g[2], g[3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (e0 + q < E) out[q] = g[q];
+        }
+      }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (adot != nullptr && ok)
+      for (int j = sub; j < k; j += LPT) {
+        const int e = topk_idx[t * k + j];
+        if (e >= 0 && e < E) extra[e] = 0.0f;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -387,34 +683,86 @@ unsigned grid_for(int64_t blocks, unsigned cap) {
 
 }  // namespace
 
+namespace {
+
+template <bool kBF16, int LPT, int VPL, int KT, int WAVES>
+unsigned launch_rows(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
+  constexpr int kTokens = WAVES * kWave / LPT, kRows = LPT <= 16 ? 4 : 1;
+  const unsigned nb = grid_for(((int64_t)a.T + kTokens - 1) / kTokens, kRouteBlocks);
+  const size_t lds = (size_t)(WAVES * kRows + 1) * a.E * 4;
+  const int vec = (int64_t)a.E * (kBF16 ? 2 : 4) % 16 == 0;
+  hipLaunchKernelGGL((route_rows<kBF16, LPT, VPL, KT, WAVES>), dim3(nb), dim3(WAVES * kWave), lds, s,
+                     a, o, vec);
+  return nb;
+}
+
+template <bool kBF16, int KT>
+unsigned launch_rows_e(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
+  if (a.E <= 128) return launch_rows<kBF16, 4, 32, KT, 8>(a, o, s);
+  if (a.E <= 256) return launch_rows<kBF16, 8, 32, KT, 8>(a, o, s);
+  if (a.E <= 512) return launch_rows<kBF16, 16, 32, KT, 4>(a, o, s);
+  return launch_rows<kBF16, 64, 64, KT, 2>(a, o, s);
+}
+
+template <bool kBF16>
+unsigned launch_rows_any(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
+  if (a.k <= 2) return launch_rows_e<kBF16, 2>(a, o, s);
+  if (a.k <= 8) return launch_rows_e<kBF16, 8>(a, o, s);
+  if (a.k <= 16) return launch_rows_e<kBF16, 16>(a, o, s);
+  // more choices than a lane's registers sort: a round of maxima per choice
+  const unsigned nb = grid_for(((int64_t)a.T + kAnyWaves - 1) / kAnyWaves, kRouteBlocks);
+  hipLaunchKernelGGL(route_any<kBF16>, dim3(nb), dim3(kAnyWaves * kWave), (size_t)kAnyWaves * a.E * 8,
+                     s, a);
+  return nb;
+}
+
+template <bool kBF16, int LPT, int VPL, int WAVES>
+void launch_back(const lrm_router& r, const void* logits, const int32_t* topk_idx,
+                 const float* topk_w, const int32_t* counts, const float* adot, float* dlogits,
+                 hipStream_t s) {
+  constexpr int kTokens = WAVES * kWave / LPT;
+  const unsigned nb = grid_for(((int64_t)r.T + kTokens - 1) / kTokens, 2048);
+  const int vec = (int64_t)r.E * (kBF16 ? 2 : 4) % 16 == 0;
+  hipLaunchKernelGGL((route_backward<kBF16, LPT, VPL, WAVES>), dim3(nb), dim3(WAVES * kWave),
+                     (size_t)kTokens * r.E * 4, s, logits, topk_idx, topk_w, counts, adot, r.T, r.E,
+                     r.k, r.gate, r.balance_coef, vec, dlogits);
+}
+
+template <bool kBF16>
+void launch_back_e(const lrm_router& r, const void* logits, const int32_t* topk_idx,
+                   const float* topk_w, const int32_t* counts, const float* adot, float* dlogits,
+                   hipStream_t s) {
+  if (r.E <= 128) return launch_back<kBF16, 4, 32, 4>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
+  if (r.E <= 256) return launch_back<kBF16, 8, 32, 4>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
+  if (r.E <= 512) return launch_back<kBF16, 16, 32, 4>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
+  launch_back<kBF16, 64, 64, 2>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
+}
+
+}  // namespace
+
 hipError_t launch_route(const lrm_router& r, const void* logits, const uint8_t* mask,
                         int32_t* topk_idx, float* topk_w, float* lse, int32_t* counts, float* prob,
                         float* loss, char* ws, hipStream_t s) {
   const RouteWs wl = route_ws(r.E);
-  RouteArgs a{logits, mask, r.T, r.E, r.k, r.gate, topk_idx, topk_w, lse,
-              (int32_t*)(ws + wl.tokens), (int32_t*)(ws + wl.counts), (float*)(ws + wl.prob)};
-  const unsigned nb = grid_for(((int64_t)r.T + kAnyWaves - 1) / kAnyWaves, kRouteBlocks);
-  const size_t lds = (size_t)kAnyWaves * r.E * 8;
-  if (r.dtype == LRM_BF16)
-    hipLaunchKernelGGL(route_any<true>, dim3(nb), dim3(kAnyWaves * kWave), lds, s, a);
-  else
-    hipLaunchKernelGGL(route_any<false>, dim3(nb), dim3(kAnyWaves * kWave), lds, s, a);
-  hipLaunchKernelGGL(route_final, dim3(1), dim3(kFinalThreads), 0, s, a.part_tokens, a.part_counts,
-                     a.part_prob, (int)nb, r.E, r.k, r.balance_coef, counts, prob, loss,
-                     (int32_t*)(ws + wl.err));
+  const RouteArgs a{logits, mask, r.T, r.E, r.k, r.gate, topk_idx, topk_w, lse,
+                    (int32_t*)(ws + wl.tokens), (int32_t*)(ws + wl.counts), (float*)(ws + wl.prob)};
+  const RouteOut o{counts, prob, loss, (int32_t*)(ws + wl.err), r.balance_coef};
+  const unsigned nb = r.dtype == LRM_BF16 ? launch_rows_any<true>(a, o, s) : launch_rows_any<false>(a, o, s);
+  // route_rows of one workgroup ends with the results themselves: one launch for a short batch
+  if (nb > 1 || r.k > 16)
+    hipLaunchKernelGGL(route_final, dim3(1), dim3(kFinalThreads), 0, s, a.part_tokens, a.part_counts,
+                       a.part_prob, (int)nb, r.E, r.k, r.balance_coef, counts, prob, loss,
+                       (int32_t*)(ws + wl.err));
   return hipGetLastError();
 }
 
 hipError_t launch_route_backward(const lrm_router& r, const void* logits, const int32_t* topk_idx,
-                                 const float* topk_w, const int32_t* counts,
-                                 const float* adot, float* dlogits, hipStream_t s) {
-  const unsigned nb = grid_for(((int64_t)r.T + kWavesPerBlock - 1) / kWavesPerBlock, 4096);
+                                 const float* topk_w, const int32_t* counts, const float* adot,
+                                 float* dlogits, hipStream_t s) {
   if (r.dtype == LRM_BF16)
-    hipLaunchKernelGGL(route_backward<true>, dim3(nb), dim3(kBlock), 0, s, logits, topk_idx, topk_w,
-                       counts, adot, r.T, r.E, r.k, r.gate, r.balance_coef, dlogits);
+    launch_back_e<true>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
   else
-    hipLaunchKernelGGL(route_backward<false>, dim3(nb), dim3(kBlock), 0, s, logits, topk_idx, topk_w,
-                       counts, adot, r.T, r.E, r.k, r.gate, r.balance_coef, dlogits);
+    launch_back_e<false>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
   return hipGetLastError();
 }
 
