@@ -187,13 +187,375 @@ __global__ __launch_bounds__(kBlock) void fc_tile(FcArgs g) {
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// bf16 products of many rows an expert.
+//
+// A workgroup of WW x WT wavefronts computes BT tokens x BW weight rows; a wavefront owns MT x NT
+// tiles of 32 x 32, the weights as the MFMA's row operand and the tokens as its columns, so a
+// lane's accumulators hold consecutive outputs of one token.  For kSwiglu the weight rows of the
+// tile are dealt in 32-row groups, gate, up, gate, up, .., so that both halves of an output column
+// meet in one lane.  Both operands contract over their contiguous axis: K steps of BK elements go
+// from global memory straight to an LDS ring of S stages (rows of BK elements, 16-byte chunks
+// XOR-swizzled so that 32 rows read at one k land on different banks), the rows of x gathered by the
+// load's per-lane offset.  A row or chunk that is not there (past the segment, past K, no valid
+// token) gets an offset beyond the buffer's range and reads as zero.
+// ------------------------------------------------------------------------------------------------
+template <int WW_, int WT_, int MT_, int NT_, int BK_, int S_>
+struct Shape {
+  static constexpr int WW = WW_, WT = WT_, MT = MT_, NT = NT_, BK = BK_, S = S_;
+  static constexpr int NW = WW * WT, THREADS = NW * kWave;
+  static constexpr int BW = 32 * MT * WW, BT = 32 * NT * WT;
+  static constexpr int ROW = BK * 2;                      // bytes of a row in LDS
+  static constexpr int CH = ROW / 16;                     // chunks of a row
+  static constexpr int SLICES = BK / 16;
+  static constexpr int T_BYTES = BT * ROW, W_BYTES = BW * ROW, STG = T_BYTES + W_BYTES;
+  static constexpr int IT = T_BYTES / 1024 / NW, IW = W_BYTES / 1024 / NW, I = IT + IW;
+  static_assert(IT * 1024 * NW == T_BYTES && IW * 1024 * NW == W_BYTES, "whole 1 KiB blocks a wave");
+  static constexpr int TABLE = 1024 + 1;                  // tiles before each expert
+  static constexpr int LDS = S * STG + (TABLE + 3) / 4 * 16;
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+// Buffer resource of 2^31 bytes from base: every offset that is used lies below what the host checked.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
+  const uint64_t v = (uint64_t)(uintptr_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), (short)0,
+                                           (int)kOutOfRange, 0x00020000);
+}
+
+// 16 bytes a lane from r + voff to LDS address lds + 16 lane.  Inline assembly, so that the compiler
+// does not wait for it before every LDS read; the pipeline orders it with vmcnt and barriers.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ bf16x8 lds_b128(uint32_t addr) {
+  return *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)addr;
+}
+
+template <class C>
+__device__ __forceinline__ int swizzle(int row) {
+  return C::CH == 8 ? row & 7 : (row >> 2) & 3;
+}
+
+// One output tile: token rows [r0, r1) of expert e, weight rows from n0.
+struct Unit {
+  int e, r0, r1, n0;
+};
+
+// Unit u of a die's range: tiles in blocks of kRowBlock row tiles, within a block rows fastest, so
+// that the workgroups of a die share a few panels of both operands at a time.
+constexpr int kRowBlock = 8;
+
+template <class C, bool kSwiglu>
+__device__ __forceinline__ Unit unit_of(const FcArgs& g, const int* before, int row_tiles, int cols,
+                                        int64_t u) {
+  const int64_t block = u / (kRowBlock * cols);
+  const int within = (int)(u - block * kRowBlock * cols);
+  const int left = row_tiles - (int)block * kRowBlock, rows = left < kRowBlock ? left : kRowBlock;
+  const int tile = (int)block * kRowBlock + within % rows;
+  int e = 0;
+  for (int e0 = 0; e0 < g.E_loc; e0 += kWave) {   // the expert whose tiles hold `tile`
+    const int lane = lane_id();
+    const uint64_t m = ballot(e0 + lane < g.E_loc && before[e0 + lane + 1] > tile);
+    if (m) {
+      e = e0 + __builtin_ctzll(m);
+      break;
+    }
+  }
+  Unit t;
+  t.e = __builtin_amdgcn_readfirstlane(e);
+  const int a = clampi(g.fwd_off[t.e], 0, g.cap), b = clampi(g.fwd_off[t.e + 1], a, g.cap);
+  t.r0 = a + (tile - before[t.e]) * C::BT;
+  t.r1 = t.r0 + C::BT < b ? t.r0 + C::BT : b;
+  t.n0 = within / rows * (kSwiglu ? C::BW / 2 : C::BW);
+  return t;
+}
+
+// Per-lane source offsets of the loads of a unit's K steps.  Lane l moves chunk `chunk` (the same for
+// all its loads) of row l / CH of each 1 KiB block.
+template <class C>
+struct Loads {
+  uint32_t t[C::IT], w[C::IW];
+};
+
+template <class C, bool kSwiglu>
+__device__ __forceinline__ void set_loads(const FcArgs& g, const Unit& u, int wave, int lane, int chunk,
+                                          Loads<C>& o) {
+  constexpr int RB = 64 / C::CH;   // rows of a block
+  const uint32_t pitch = (uint32_t)g.K * 2;
+#pragma unroll
+  for (int j = 0; j < C::IT; ++j) {
+    const int r = u.r0 + (wave * C::IT + j) * RB + lane / C::CH;
+    uint32_t off = kOutOfRange;
+    if (r < u.r1) {
+      if (kSwiglu) {
+        const int p = g.row_pair[r];
+        if (p >= 0 && p < g.P)
+          off = (uint32_t)(p / g.k) * pitch + chunk * 16;
+        else
+          set_error(g.err, LRM_DEVERR_INDEX);
+      } else {
+        off = (uint32_t)(r - u.r0) * pitch + chunk * 16;
+      }
+    }
+    o.t[j] = off;
+  }
+#pragma unroll
+  for (int j = 0; j < C::IW; ++j) {
+    const int row = (wave * C::IW + j) * RB + lane / C::CH;
+    const int col = u.n0 + (kSwiglu ? row / 64 * 32 + row % 32 : row);
+    const uint32_t src = kSwiglu && (row & 32) ? (uint32_t)(g.N + col) : (uint32_t)col;
+    o.w[j] = col < g.N ? src * pitch + chunk * 16 : kOutOfRange;
+  }
+}
+
+// The loads of the K step at k0 into the stage at LDS address `st`, and the bases they start from.
+template <class C>
+struct Stream {
+  const char* pt;   // tokens, advanced by a K step at a time
+  const char* pw;
+  int k0;
+};
+
+template <class C>
+__device__ __forceinline__ void fire(Stream<C>& s, const Loads<C>& o, int K, int chunk, uint32_t st,
+                                     int wave) {
+  const __amdgpu_buffer_rsrc_t rt = operand(s.pt), rw = operand(s.pw);
+  const uint32_t lt = st + wave * C::IT * 1024, lw = st + C::T_BYTES + wave * C::IW * 1024;
+  if (s.k0 + C::BK <= K) {
+#pragma unroll
+    for (int j = 0; j < C::IT; ++j) dma16(rt, lt + j * 1024, o.t[j]);
+#pragma unroll
+    for (int j = 0; j < C::IW; ++j) dma16(rw, lw + j * 1024, o.w[j]);
+  } else {
+    const bool in = s.k0 + chunk * 8 < K;
+#pragma unroll
+    for (int j = 0; j < C::IT; ++j) dma16(rt, lt + j * 1024, in ? o.t[j] : kOutOfRange);
+#pragma unroll
+    for (int j = 0; j < C::IW; ++j) dma16(rw, lw + j * 1024, in ? o.w[j] : kOutOfRange);
+  }
+  s.pt += C::ROW;
+  s.pw += C::ROW;
+  s.k0 += C::BK;
+}
+
+template <class C>
+struct Frags {
+  bf16x8 w[C::MT], t[C::NT];
+};
+
+// Lane offsets (bytes from a stage) of this wavefront's fragments of each 16-wide slice.
+template <class C>
+struct Reads {
+  uint32_t w[C::SLICES], t[C::SLICES];
+};
+
+template <class C>
+__device__ __forceinline__ void read_frags(Frags<C>& f, const Reads<C>& r, uint32_t st, int slice) {
+  const uint32_t pw = st + r.w[slice], pt = st + r.t[slice];
+#pragma unroll
+  for (int i = 0; i < C::MT; ++i) f.w[i] = lds_b128(pw + i * 32 * C::ROW);
+#pragma unroll
+  for (int j = 0; j < C::NT; ++j) f.t[j] = lds_b128(pt + j * 32 * C::ROW);
+}
+
+template <class C>
+__device__ __forceinline__ void multiply(const Frags<C>& f, f32x16 (&acc)[C::MT][C::NT]) {
+#pragma unroll
+  for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NT; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.w[i], f.t[j], acc[i][j], 0, 0, 0);
+}
+
+// Spreads the slice's LDS reads over its MFMAs.
+template <class C>
+__device__ __forceinline__ void interleave() {
+  static_assert(C::MT + C::NT <= C::MT * C::NT, "a read behind each MFMA");
+#pragma unroll
+  for (int q = 0; q < C::MT * C::NT; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+}
+
+// 8 outputs of one token per lane and 16-column group: accumulators hold columns 8 g + 4 (l / 32)
+// + 0..3 of token l % 32 for g = 0..3; the halves of two groups change places between lanes l and
+// l + 32, so that each lane has 8 consecutive columns to store in one 16-byte access.
+__device__ __forceinline__ void store_tile(uint16_t* row, int col, int N, int lane, const float (&v)[16]) {
+  uint32_t p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const auto x = __builtin_amdgcn_permlane32_swap(p[4 * h + i], p[4 * h + 2 + i], false, false);
+      q[i] = x[0];
+      q[2 + i] = x[1];
+    }
+    const int c = col + 16 * h + 8 * (lane >> 5);
+    if (row != nullptr && c < N) *(uint4*)(row + c) = make_uint4(q[0], q[1], q[2], q[3]);
+  }
+}
+
+template <class C, bool kSwiglu>
+__global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  int* before = (int*)(lds + C::S * C::STG);
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int ww = wave / C::WT, wt = wave % C::WT;
+  // tiles before each expert
+  if (wave == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < g.E_loc; e0 += kWave) {
+      const int e = e0 + lane;
+      int n = 0;
+      if (e < g.E_loc) {
+        const int a = clampi(g.fwd_off[e], 0, g.cap), b = clampi(g.fwd_off[e + 1], a, g.cap);
+        n = (b - a + C::BT - 1) / C::BT;
+      }
+      const int inc = wave_inclusive_scan(n);
+      if (e < g.E_loc) before[e + 1] = base + inc;
+      base += __shfl(inc, kWave - 1, kWave);
+    }
+    if (lane == 0) before[0] = 0;
+  }
+  __syncthreads();
+  const int row_tiles = __builtin_amdgcn_readfirstlane(before[g.E_loc]);
+  const int bn = kSwiglu ? C::BW / 2 : C::BW, cols = (g.N + bn - 1) / bn;
+  const int64_t total = (int64_t)row_tiles * cols, per = (total + nxcd - 1) / nxcd;
+  const int64_t lo = (int64_t)(blockIdx.x % nxcd) * per, hi = lo + per < total ? lo + per : total;
+  const int nb = gridDim.x / nxcd;
+
+  const uint32_t ring = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds);
+  Reads<C> rd;
+#pragma unroll
+  for (int s = 0; s < C::SLICES; ++s) {
+    const uint32_t at = (lane & 31) * C::ROW + (((2 * s + (lane >> 5)) ^ swizzle<C>(lane & 31)) << 4);
+    rd.w[s] = C::T_BYTES + ww * C::MT * 32 * C::ROW + at;
+    rd.t[s] = wt * C::NT * 32 * C::ROW + at;
+  }
+  const int chunk = (lane % C::CH) ^ swizzle<C>(lane / C::CH);
+  const int nk = (g.K + C::BK - 1) / C::BK;
+  for (int64_t u = lo + blockIdx.x / nxcd; u < hi; u += nb) {
+    const Unit t = unit_of<C, kSwiglu>(g, before, row_tiles, cols, u);
+    Loads<C> o;
+    set_loads<C, kSwiglu>(g, t, wave, lane, chunk, o);
+    Stream<C> st;
+    st.pt = (const char*)g.A + (kSwiglu ? 0 : (int64_t)t.r0 * g.K * 2);
+    st.pw = (const char*)g.B + (int64_t)t.e * (kSwiglu ? 2 : 1) * g.N * g.K * 2;
+    st.k0 = 0;
+#pragma unroll
+    for (int s = 0; s < C::S; ++s)
+      fire<C>(st, o, g.K, chunk, ring + s * C::STG, wave);
+    f32x16 acc[C::MT][C::NT];
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+    wait_vm<(C::S - 1) * C::I>();
+    lds_barrier();
+    uint32_t cur = ring;
+    Frags<C> f[2];
+    read_frags<C>(f[0], rd, cur, 0);
+    for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+      for (int s = 0; s + 1 < C::SLICES; ++s) {
+        read_frags<C>(f[(s + 1) & 1], rd, cur, s + 1);
+        multiply<C>(f[s & 1], acc);
+        interleave<C>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // every fragment of this stage is in registers: once all waves are here it may be refilled;
+      // the next stage has landed for every wave
+      wait_vm<(C::S - 2) * C::I>();
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of the stage are done
+      lds_barrier();
+      const uint32_t next = cur + C::STG == ring + C::S * C::STG ? ring : cur + C::STG;
+      __builtin_amdgcn_sched_barrier(0);
+      fire<C>(st, o, g.K, chunk, cur, wave);
+      __builtin_amdgcn_sched_barrier(0);
+      read_frags<C>(f[C::SLICES & 1], rd, next, 0);
+      multiply<C>(f[(C::SLICES - 1) & 1], acc);
+      interleave<C>();
+      __builtin_amdgcn_sched_barrier(0);
+      cur = next;
+    }
+    wait_vm<0>();
+    lds_barrier();
+#pragma unroll
+    for (int j = 0; j < C::NT; ++j) {
+      const int64_t r = t.r0 + (wt * C::NT + j) * 32 + (lane & 31);
+      const bool in = r < t.r1;
+#pragma unroll
+      for (int i = 0; i < C::MT; i += kSwiglu ? 2 : 1) {
+        float v[16];
+        if constexpr (kSwiglu) {
+          const int col = t.n0 + (ww * C::MT + i) * 16;
+          uint16_t* ac = in && g.out != nullptr ? (uint16_t*)g.out + r * 2 * g.N : nullptr;
+          if (g.out != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
+            store_tile(ac, col, g.N, lane, v);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = acc[i + 1][j][q];
+            store_tile(ac != nullptr ? ac + g.N : nullptr, col, g.N, lane, v);
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) v[q] = silu_mul(acc[i][j][q], acc[i + 1][j][q]);
+          store_tile(in ? (uint16_t*)g.out2 + r * g.N : nullptr, col, g.N, lane, v);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
+          store_tile(in ? (uint16_t*)g.out + r * g.N : nullptr, t.n0 + (ww * C::MT + i) * 32, g.N, lane, v);
+        }
+      }
+    }
+  }
+}
+
+// Workgroups of the persistent products: one a CU, a multiple of the dies.
+constexpr int kDies = 8, kCUs = 256;
+
+#ifndef LRM_FC_SHAPE
+#define LRM_FC_SHAPE 4, 2, 2, 4, 64, 2
+#endif
+
 template <bool kSwiglu>
 hipError_t launch_fc(const lrm_problem& p, const FcArgs& g, hipStream_t s) {
   const int bn = kSwiglu ? kBNH : 2 * kBNH;
   // every expert's last tile may be partial
   const int64_t units = (((int64_t)p.L_cap + kBM - 1) / kBM + p.E_loc) * ((g.N + bn - 1) / bn);
   const dim3 grid((unsigned)(units < (1 << 20) ? units : 1 << 20));
-  if (p.dtype == LRM_BF16)
+  using Big = Shape<LRM_FC_SHAPE>;
+  if (p.dtype == LRM_BF16 && p.L_cap >= 128 * p.E_loc)
+    hipLaunchKernelGGL((fc_bf16<Big, kSwiglu>), dim3(kCUs), dim3(Big::THREADS), 0, s, g, kDies);
+  else if (p.dtype == LRM_BF16)
     hipLaunchKernelGGL((fc_tile<true, kSwiglu>), grid, dim3(kBlock), 0, s, g);
   else
     hipLaunchKernelGGL((fc_tile<false, kSwiglu>), grid, dim3(kBlock), 0, s, g);
