@@ -200,13 +200,15 @@ __global__ __launch_bounds__(kBlock) void fc_tile(FcArgs g) {
 // load's per-lane offset.  A row or chunk that is not there (past the segment, past K, no valid
 // token) gets an offset beyond the buffer's range and reads as zero.
 // ------------------------------------------------------------------------------------------------
-template <int WW_, int WT_, int MT_, int NT_, int BK_, int S_>
+constexpr int BK = 64;                                    // K step: rows of 128 bytes in LDS
+constexpr int CH = 8;                                     // their 16-byte chunks
+
+template <int WW_, int WT_, int MT_, int NT_, int S_>
 struct Shape {
-  static constexpr int WW = WW_, WT = WT_, MT = MT_, NT = NT_, BK = BK_, S = S_;
+  static constexpr int WW = WW_, WT = WT_, MT = MT_, NT = NT_, S = S_;
   static constexpr int NW = WW * WT, THREADS = NW * kWave;
   static constexpr int BW = 32 * MT * WW, BT = 32 * NT * WT;
   static constexpr int ROW = BK * 2;                      // bytes of a row in LDS
-  static constexpr int CH = ROW / 16;                     // chunks of a row
   static constexpr int SLICES = BK / 16;
   static constexpr int T_BYTES = BT * ROW, W_BYTES = BW * ROW, STG = T_BYTES + W_BYTES;
   static constexpr int IT = T_BYTES / 1024 / NW, IW = W_BYTES / 1024 / NW, I = IT + IW;
@@ -252,10 +254,11 @@ __device__ __forceinline__ bf16x8 lds_b128(uint32_t addr) {
   return *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)addr;
 }
 
-template <class C>
-__device__ __forceinline__ int swizzle(int row) {
-  return C::CH == 8 ? row & 7 : (row >> 2) & 3;
-}
+// Chunk c of row r sits at chunk c ^ swizzle(r).  Two rows span the 64 banks, so any 16 rows that
+// hold each value of (r / 2) % 8 twice, once in an even and once in an odd row, read 16 different
+// 16-byte groups of banks at one k: so do the 16 lanes that a 16-byte LDS read serves at a time.
+// (r % 8 instead would put rows r and r + 8 on the same banks: half of all LDS cycles were conflicts.)
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 
 // One output tile: token rows [r0, r1) of expert e, weight rows from n0.
 struct Unit {
@@ -291,73 +294,86 @@ __device__ __forceinline__ Unit unit_of(const FcArgs& g, const int* before, int 
   return t;
 }
 
-// Per-lane source offsets of the loads of a unit's K steps.  Lane l moves chunk `chunk` (the same for
-// all its loads) of row l / CH of each 1 KiB block.
-template <class C>
-struct Loads {
-  uint32_t t[C::IT], w[C::IW];
-};
-
+// The loads, which run ahead of the products through the K steps of one unit and on into the next:
+// a unit's epilogue and the next one's first loads then take place together.  Per lane: the source
+// offset of each 16 bytes it moves, constant over a unit's K steps (the bases advance); lane l moves
+// a chunk of row l / 8 of each 1 KiB block of 8 rows, chunk_of(q) in block q.
 template <class C, bool kSwiglu>
-__device__ __forceinline__ void set_loads(const FcArgs& g, const Unit& u, int wave, int lane, int chunk,
-                                          Loads<C>& o) {
-  constexpr int RB = 64 / C::CH;   // rows of a block
-  const uint32_t pitch = (uint32_t)g.K * 2;
+struct Loader {
+  uint32_t t[C::IT], w[C::IW];
+  int pair[C::IT];       // the rows' pairs, fetched one step before the offsets are formed
+  const char* pt;        // tokens and weights at k0
+  const char* pw;
+  int k0, wave, lane;
+  bool more;             // a unit is left to load
+
+  // the chunk that belongs at position l % 8 of row 8 q + l / 8
+  __device__ __forceinline__ int chunk_of(int q) const {
+    return (lane % CH) ^ (lane / 16) ^ ((q & 1) << 2);
+  }
+
+  __device__ __forceinline__ void fetch(const FcArgs& g, const Unit& u) {
+    if constexpr (kSwiglu) {
 #pragma unroll
-  for (int j = 0; j < C::IT; ++j) {
-    const int r = u.r0 + (wave * C::IT + j) * RB + lane / C::CH;
-    uint32_t off = kOutOfRange;
-    if (r < u.r1) {
-      if (kSwiglu) {
-        const int p = g.row_pair[r];
-        if (p >= 0 && p < g.P)
-          off = (uint32_t)(p / g.k) * pitch + chunk * 16;
-        else
-          set_error(g.err, LRM_DEVERR_INDEX);
-      } else {
-        off = (uint32_t)(r - u.r0) * pitch + chunk * 16;
+      for (int j = 0; j < C::IT; ++j) {
+        const int r = u.r0 + (wave * C::IT + j) * CH + lane / CH;
+        pair[j] = r < u.r1 ? g.row_pair[r] : 0;
       }
     }
-    o.t[j] = off;
   }
-#pragma unroll
-  for (int j = 0; j < C::IW; ++j) {
-    const int row = (wave * C::IW + j) * RB + lane / C::CH;
-    const int col = u.n0 + (kSwiglu ? row / 64 * 32 + row % 32 : row);
-    const uint32_t src = kSwiglu && (row & 32) ? (uint32_t)(g.N + col) : (uint32_t)col;
-    o.w[j] = col < g.N ? src * pitch + chunk * 16 : kOutOfRange;
-  }
-}
 
-// The loads of the K step at k0 into the stage at LDS address `st`, and the bases they start from.
-template <class C>
-struct Stream {
-  const char* pt;   // tokens, advanced by a K step at a time
-  const char* pw;
-  int k0;
+  __device__ __forceinline__ void begin(const FcArgs& g, const Unit& u) {
+    const uint32_t pitch = (uint32_t)g.K * 2;
+#pragma unroll
+    for (int j = 0; j < C::IT; ++j) {
+      const int r = u.r0 + (wave * C::IT + j) * CH + lane / CH;
+      if constexpr (kSwiglu) {
+        const bool ok = pair[j] >= 0 && pair[j] < g.P;
+        if (!ok) set_error(g.err, LRM_DEVERR_INDEX);
+        t[j] = r < u.r1 && ok ? (uint32_t)(pair[j] / g.k) * pitch + chunk_of(wave * C::IT + j) * 16
+                              : kOutOfRange;
+      } else {
+        t[j] = r < u.r1 ? (uint32_t)(r - u.r0) * pitch + chunk_of(wave * C::IT + j) * 16 : kOutOfRange;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < C::IW; ++j) {
+      const int row = (wave * C::IW + j) * CH + lane / CH;
+      const int col = u.n0 + (kSwiglu ? row / 64 * 32 + row % 32 : row);
+      const uint32_t src = kSwiglu && (row & 32) ? (uint32_t)(g.N + col) : (uint32_t)col;
+      w[j] = col < g.N ? src * pitch + chunk_of(wave * C::IW + j) * 16 : kOutOfRange;
+    }
+    pt = (const char*)g.A + (kSwiglu ? 0 : (int64_t)u.r0 * g.K * 2);
+    pw = (const char*)g.B + (int64_t)u.e * (kSwiglu ? 2 : 1) * g.N * g.K * 2;
+    k0 = 0;
+  }
+
+  // Load q (tokens first) of the K step at k0 into the stage at LDS address `st`; where the step ends
+  // past K, the chunks past it become zeros.
+  template <int Q>
+  __device__ __forceinline__ void load(uint32_t st, __amdgpu_buffer_rsrc_t rt, __amdgpu_buffer_rsrc_t rw,
+                                       int K) const {
+    const int q = Q < C::IT ? wave * C::IT + Q : wave * C::IW + Q - C::IT;
+    uint32_t off;
+    if constexpr (Q < C::IT) off = t[Q];
+    else off = w[Q - C::IT];
+    if (k0 + BK > K) off = k0 + chunk_of(q) * 8 < K ? off : kOutOfRange;
+    dma16(Q < C::IT ? rt : rw, st + (Q < C::IT ? 0 : C::T_BYTES) + q * 1024, off);
+  }
+  template <int Q = 0>
+  __device__ __forceinline__ void load_all(uint32_t st, __amdgpu_buffer_rsrc_t rt, __amdgpu_buffer_rsrc_t rw,
+                                           int K) const {
+    if constexpr (Q < C::I) {
+      load<Q>(st, rt, rw, K);
+      load_all<Q + 1>(st, rt, rw, K);
+    }
+  }
+  __device__ __forceinline__ void step() {
+    pt += C::ROW;
+    pw += C::ROW;
+    k0 += BK;
+  }
 };
-
-template <class C>
-__device__ __forceinline__ void fire(Stream<C>& s, const Loads<C>& o, int K, int chunk, uint32_t st,
-                                     int wave) {
-  const __amdgpu_buffer_rsrc_t rt = operand(s.pt), rw = operand(s.pw);
-  const uint32_t lt = st + wave * C::IT * 1024, lw = st + C::T_BYTES + wave * C::IW * 1024;
-  if (s.k0 + C::BK <= K) {
-#pragma unroll
-    for (int j = 0; j < C::IT; ++j) dma16(rt, lt + j * 1024, o.t[j]);
-#pragma unroll
-    for (int j = 0; j < C::IW; ++j) dma16(rw, lw + j * 1024, o.w[j]);
-  } else {
-    const bool in = s.k0 + chunk * 8 < K;
-#pragma unroll
-    for (int j = 0; j < C::IT; ++j) dma16(rt, lt + j * 1024, in ? o.t[j] : kOutOfRange);
-#pragma unroll
-    for (int j = 0; j < C::IW; ++j) dma16(rw, lw + j * 1024, in ? o.w[j] : kOutOfRange);
-  }
-  s.pt += C::ROW;
-  s.pw += C::ROW;
-  s.k0 += C::BK;
-}
 
 template <class C>
 struct Frags {
@@ -454,23 +470,43 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
   Reads<C> rd;
 #pragma unroll
   for (int s = 0; s < C::SLICES; ++s) {
-    const uint32_t at = (lane & 31) * C::ROW + (((2 * s + (lane >> 5)) ^ swizzle<C>(lane & 31)) << 4);
+    const uint32_t at = (lane & 31) * C::ROW + (((2 * s + (lane >> 5)) ^ swizzle(lane & 31)) << 4);
     rd.w[s] = C::T_BYTES + ww * C::MT * 32 * C::ROW + at;
     rd.t[s] = wt * C::NT * 32 * C::ROW + at;
   }
-  const int chunk = (lane % C::CH) ^ swizzle<C>(lane / C::CH);
-  const int nk = (g.K + C::BK - 1) / C::BK;
-  for (int64_t u = lo + blockIdx.x / nxcd; u < hi; u += nb) {
-    const Unit t = unit_of<C, kSwiglu>(g, before, row_tiles, cols, u);
-    Loads<C> o;
-    set_loads<C, kSwiglu>(g, t, wave, lane, chunk, o);
-    Stream<C> st;
-    st.pt = (const char*)g.A + (kSwiglu ? 0 : (int64_t)t.r0 * g.K * 2);
-    st.pw = (const char*)g.B + (int64_t)t.e * (kSwiglu ? 2 : 1) * g.N * g.K * 2;
-    st.k0 = 0;
-#pragma unroll
-    for (int s = 0; s < C::S; ++s)
-      fire<C>(st, o, g.K, chunk, ring + s * C::STG, wave);
+  int64_t u = lo + blockIdx.x / nxcd;
+  if (u >= hi) return;
+  Loader<C, kSwiglu> ld;
+  ld.wave = wave;
+  ld.lane = lane;
+  const int nk = (g.K + BK - 1) / BK;
+  Unit t = unit_of<C, kSwiglu>(g, before, row_tiles, cols, u), nx = t;
+  int64_t un = u;        // the loader's unit
+  ld.fetch(g, t);
+  ld.begin(g, t);
+  ld.more = true;
+  // the first S steps of the stream
+  for (int s = 0; s < C::S; ++s) {
+    if (ld.more) {
+      ld.load_all(ring + s * C::STG, operand(ld.pt), operand(ld.pw), g.K);
+      ld.step();
+      if (ld.k0 >= g.K) {
+        un += nb;
+        ld.more = un < hi;
+        if (ld.more) {
+          nx = unit_of<C, kSwiglu>(g, before, row_tiles, cols, un);
+          ld.fetch(g, nx);
+          ld.begin(g, nx);
+        }
+      }
+    }
+  }
+  wait_vm<0>();
+  lds_barrier();
+  uint32_t cur = ring;
+  Frags<C> f[2];
+  read_frags<C>(f[0], rd, cur, 0);
+  for (; u < hi; u += nb) {
     f32x16 acc[C::MT][C::NT];
 #pragma unroll
     for (int i = 0; i < C::MT; ++i)
@@ -478,11 +514,6 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
       for (int j = 0; j < C::NT; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-    wait_vm<(C::S - 1) * C::I>();
-    lds_barrier();
-    uint32_t cur = ring;
-    Frags<C> f[2];
-    read_frags<C>(f[0], rd, cur, 0);
     for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
       for (int s = 0; s + 1 < C::SLICES; ++s) {
@@ -493,12 +524,28 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
       }
       // every fragment of this stage is in registers: once all waves are here it may be refilled;
       // the next stage has landed for every wave
-      wait_vm<(C::S - 2) * C::I>();
+      if (C::S > 2 && ld.more)
+        wait_vm<(C::S - 2) * C::I>();
+      else
+        wait_vm<0>();
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of the stage are done
       lds_barrier();
       const uint32_t next = cur + C::STG == ring + C::S * C::STG ? ring : cur + C::STG;
+      if (ld.more && ld.k0 >= g.K) ld.begin(g, nx);
       __builtin_amdgcn_sched_barrier(0);
-      fire<C>(st, o, g.K, chunk, cur, wave);
+      if (ld.more) {
+        const __amdgpu_buffer_rsrc_t rt = operand(ld.pt), rw = operand(ld.pw);
+        ld.load_all(cur, rt, rw, g.K);
+        ld.step();
+        if (ld.k0 >= g.K) {   // the unit's last loads are out: its successor's rows
+          un += nb;
+          ld.more = un < hi;
+          if (ld.more) {
+            nx = unit_of<C, kSwiglu>(g, before, row_tiles, cols, un);
+            ld.fetch(g, nx);
+          }
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
       read_frags<C>(f[C::SLICES & 1], rd, next, 0);
       multiply<C>(f[(C::SLICES - 1) & 1], acc);
@@ -506,8 +553,6 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
       __builtin_amdgcn_sched_barrier(0);
       cur = next;
     }
-    wait_vm<0>();
-    lds_barrier();
 #pragma unroll
     for (int j = 0; j < C::NT; ++j) {
       const int64_t r = t.r0 + (wt * C::NT + j) * 32 + (lane & 31);
@@ -536,6 +581,8 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
         }
       }
     }
+    // the loader is in the next unit, unless units are so short that it is past it already
+    if (u + nb < hi) t = nk > C::S ? nx : unit_of<C, kSwiglu>(g, before, row_tiles, cols, u + nb);
   }
 }
 
@@ -543,7 +590,7 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
 constexpr int kDies = 8, kCUs = 256;
 
 #ifndef LRM_FC_SHAPE
-#define LRM_FC_SHAPE 4, 2, 2, 4, 64, 2
+#define LRM_FC_SHAPE 4, 2, 2, 4, 2
 #endif
 
 template <bool kSwiglu>
