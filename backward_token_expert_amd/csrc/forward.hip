@@ -6,6 +6,7 @@
 // whose backward the other calls compute).  Both products contract over the contiguous axis of
 // both operands (rows of x or phi against rows of W1 or W).
 #include <math.h>
+#include <stdlib.h>
 
 #include "lrm_device.hpp"
 #include "lrm_forward.hpp"
@@ -586,6 +587,200 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// Few rows an expert (serving steps): bound by streaming the chosen experts' weights once.
+//
+// A workgroup computes up to 16 TT tokens x 32 weight rows (for kSwiglu 16 of each half) of one expert; its four wavefronts share the contracted axis, 128 bytes of every row in turn, so that
+// even one token's eight experts put thousands of wavefronts' loads in flight at once.  Nothing
+// goes through LDS but the four partial sums, added in a fixed order: a 16-row MFMA operand is one
+// 16-byte load a lane (16 rows x 64 bytes), which for float32 serves four MFMAs, lane group q
+// holding k = 4 q + i for the i-th (any order of k will do, as both operands have the same).
+// Rows past the segment's end read its last row again and are not stored.
+// ------------------------------------------------------------------------------------------------
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+constexpr int kFewWaves = 4;
+#ifndef FEW_R
+#define FEW_R 5
+#endif
+#ifndef FEW_A
+#define FEW_A 2, 1
+#define FEW_B 4, 2
+#define FEW_N 2
+#endif
+constexpr int kFewAhead = FEW_N;   // 128-byte pieces of each row in flight per wavefront
+
+template <bool kBF16>
+__device__ __forceinline__ f32x4 few_mma(uint4 a, uint4 b, f32x4 c) {
+  if constexpr (kBF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else {
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  }
+}
+
+// The token of pair p, or -1 for a pair id that is none.
+__device__ __forceinline__ int64_t token_of(const FcArgs& g, int p) {
+  return p >= 0 && p < g.P ? p / g.k : -1;
+}
+
+// 128 bytes of 2 x 16 weight rows and TT x 16 token rows.
+template <int WF, int TT>
+struct FewPiece {
+  uint4 a[2][WF], b[2][TT];
+  __device__ __forceinline__ void load(const char* const (&pw)[WF], const char* const (&pt)[TT], int64_t off) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < WF; ++i) a[h][i] = load_nt((const uint4*)(pw[i] + off + 64 * h));
+#pragma unroll
+      for (int j = 0; j < TT; ++j) b[h][j] = *(const uint4*)(pt[j] + off + 64 * h);
+    }
+  }
+  // the last, partial piece: `left` elements from this lane's first, `half` of them 64 bytes on
+  __device__ __forceinline__ void load_rest(const char* const (&pw)[WF], const char* const (&pt)[TT],
+                                            int64_t off, int left, int half) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = left > h * half;
+#pragma unroll
+      for (int i = 0; i < WF; ++i) a[h][i] = in ? *(const uint4*)(pw[i] + off + 64 * h) : zero;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) b[h][j] = in ? *(const uint4*)(pt[j] + off + 64 * h) : zero;
+    }
+  }
+  template <bool kBF16>
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[WF][TT]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < WF; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[i][j] = few_mma<kBF16>(a[h][i], b[h][j], acc[i][j]);
+  }
+};
+
+template <bool kBF16, bool kSwiglu, int WF, int TT>
+__global__ __launch_bounds__(kFewWaves * kWave) void fc_few(FcArgs g) {
+  constexpr int ESZ = kBF16 ? 2 : 4, V = 16 / ESZ;
+  constexpr int STEP = 128 / ESZ;              // contracted elements of a 128-byte piece
+  constexpr int BN = kSwiglu ? 8 * WF : 16 * WF;   // output columns
+  __shared__ f32x4 part[kFewWaves][WF * TT][kWave];
+  const int lane = lane_id(), w = threadIdx.x / kWave;
+  const int cols = (g.N + BN - 1) / BN;
+  for (int64_t u = blockIdx.x;; u += gridDim.x) {
+    const RowTile t = find_tile<16 * TT>(g.fwd_off, g.E_loc, g.cap, (int)(u / cols));
+    if (t.e < 0) return;
+    const int n0 = (int)(u % cols) * BN;
+    const int64_t K = g.K;
+    const int k0 = (lane >> 4) * V;            // this lane's elements of a 64-byte half piece
+    const char* pw[WF];
+    const char* pt[TT];
+#pragma unroll
+    for (int i = 0; i < WF; ++i) {
+      // columns past the last one read it again
+      const int c = n0 + 16 * (kSwiglu ? i / 2 : i) + (lane & 15);
+      const int64_t row = (c < g.N ? c : g.N - 1) + (kSwiglu && i % 2 ? (int64_t)g.N : 0);
+      pw[i] = (const char*)g.B + ((int64_t)t.e * (kSwiglu ? 2 : 1) * g.N + row) * K * ESZ + k0 * ESZ;
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      int64_t r = t.r0 + 16 * j + (lane & 15);
+      r = r < t.r1 ? r : t.r1 - 1;
+      if (kSwiglu) r = token_of(g, g.row_pair[r]);
+      pt[j] = (const char*)g.A + ((r < 0 ? 0 : r) * K + k0) * ESZ;   // a bad pair's outputs: below
+    }
+    f32x4 acc[WF][TT];
+#pragma unroll
+    for (int i = 0; i < WF; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    // whole 128-byte pieces of the rows, this wavefront's w, w + 4, ..; then the row's rest
+    const int whole = g.K / STEP;
+    FewPiece<WF, TT> f[kFewAhead];
+    if (whole > 0) {
+      // the loads run ahead without a condition, so that each wait is for one piece's loads alone;
+      // past the end they fetch the last piece again
+      const int last = whole - 1, turn = (int)(u * FEW_R % whole);
+      auto at = [&](int c) {
+        c = (c < last ? c : last) + turn;
+        return (int64_t)(c < whole ? c : c - whole) * 128;
+      };
+#pragma unroll
+      for (int q = 0; q < kFewAhead; ++q) {
+        const int c = w + q * kFewWaves;
+        f[q].load(pw, pt, at(c));
+      }
+      for (int c = w; c < whole; c += kFewAhead * kFewWaves) {
+#pragma unroll
+        for (int q = 0; q < kFewAhead; ++q) {
+          if (c + q * kFewWaves < whole) f[q].template multiply<kBF16>(acc);
+          const int next = c + (kFewAhead + q) * kFewWaves;
+          f[q].load(pw, pt, at(next));
+        }
+      }
+    }
+    if (g.K % STEP && whole % kFewWaves == w) {
+      f[0].load_rest(pw, pt, (int64_t)whole * 128, g.K - whole * STEP - k0, STEP / 2);
+      f[0].template multiply<kBF16>(acc);
+    }
+#pragma unroll
+    for (int i = 0; i < WF; ++i)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) part[w][i * TT + j][lane] = acc[i][j];
+    __syncthreads();
+    // the (column, token) fragments are ended by the wavefronts in turn: lane l holds columns
+    // 4 (l / 16) + 0..3 of token l % 16
+    constexpr int OF = kSwiglu ? WF / 2 : WF;   // output fragments along the columns
+    for (int o = w; o < OF * TT; o += kFewWaves) {
+      const int ci = o / TT, ti = o % TT;
+      const int64_t r = t.r0 + 16 * ti + (lane & 15);
+      f32x4 v = part[0][(kSwiglu ? 2 * ci : ci) * TT + ti][lane], x = v;
+#pragma unroll
+      for (int q = 1; q < kFewWaves; ++q) v += part[q][(kSwiglu ? 2 * ci : ci) * TT + ti][lane];
+      if constexpr (kSwiglu) {
+        x = part[0][(2 * ci + 1) * TT + ti][lane];
+#pragma unroll
+        for (int q = 1; q < kFewWaves; ++q) x += part[q][(2 * ci + 1) * TT + ti][lane];
+      }
+      if (r < t.r1) {
+        if (kSwiglu && token_of(g, g.row_pair[r]) < 0) {   // reads x as zeros
+          v = x = (f32x4){0.f, 0.f, 0.f, 0.f};
+          set_error(g.err, LRM_DEVERR_INDEX);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = n0 + 16 * ci + 4 * (lane >> 4) + i;
+          if (c >= g.N) continue;
+          if constexpr (kSwiglu) {
+            if (g.out != nullptr) {
+              store_elem<kBF16>(g.out, r * 2 * g.N + c, v[i]);
+              store_elem<kBF16>(g.out, r * 2 * g.N + g.N + c, x[i]);
+            }
+            store_elem<kBF16>(g.out2, r * g.N + c, silu_mul(v[i], x[i]));
+          } else {
+            store_elem<kBF16>(g.out, r * g.N + c, v[i]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <bool kBF16, bool kSwiglu, int WF, int TT>
+void launch_few(const lrm_problem& p, const FcArgs& g, hipStream_t s) {
+  const int bn = kSwiglu ? 8 * WF : 16 * WF, rows = 16 * TT;
+  const int64_t most = (int64_t)p.L_cap / rows + p.E_loc;   // tiles, if every expert's last is partial
+  const int64_t units = (most < p.L_cap ? most : p.L_cap) * ((g.N + bn - 1) / bn);
+  hipLaunchKernelGGL((fc_few<kBF16, kSwiglu, WF, TT>), dim3((unsigned)(units < (1 << 20) ? units : 1 << 20)),
+                     dim3(kFewWaves * kWave), 0, s, g);
+}
+
 // Workgroups of the persistent products: one a CU, a multiple of the dies.
 constexpr int kDies = 8, kCUs = 256;
 
@@ -600,7 +795,17 @@ hipError_t launch_fc(const lrm_problem& p, const FcArgs& g, hipStream_t s) {
   const int64_t units = (((int64_t)p.L_cap + kBM - 1) / kBM + p.E_loc) * ((g.N + bn - 1) / bn);
   const dim3 grid((unsigned)(units < (1 << 20) ? units : 1 << 20));
   using Big = Shape<LRM_FC_SHAPE>;
-  if (p.dtype == LRM_BF16 && p.L_cap >= 128 * p.E_loc)
+  const int few = getenv("LRM_FEW") ? atoi(getenv("LRM_FEW")) : 16;
+  if (p.L_cap <= (int64_t)few * p.E_loc) {
+    const bool one = p.L_cap <= 4 * (int64_t)p.E_loc;
+    if (p.dtype == LRM_BF16) {
+      if (one) launch_few<true, kSwiglu, FEW_A>(p, g, s);
+      else launch_few<true, kSwiglu, FEW_B>(p, g, s);
+    } else {
+      if (one) launch_few<false, kSwiglu, FEW_A>(p, g, s);
+      else launch_few<false, kSwiglu, FEW_B>(p, g, s);
+    }
+  } else if (p.dtype == LRM_BF16 && p.L_cap >= (getenv("LRM_BIG") ? atoi(getenv("LRM_BIG")) : 128) * (int64_t)p.E_loc)
     hipLaunchKernelGGL((fc_bf16<Big, kSwiglu>), dim3(kCUs), dim3(Big::THREADS), 0, s, g, kDies);
   else if (p.dtype == LRM_BF16)
     hipLaunchKernelGGL((fc_tile<true, kSwiglu>), grid, dim3(kBlock), 0, s, g);
@@ -652,12 +857,14 @@ struct Chunk<false> {
   }
 };
 
-// One wavefront per token: the rows of its local pairs through the map (an entry counts only if it
-// points inside [0, L) at a row that names the pair, so stale entries are ignored), summed in slot
-// order in float32, kC 16-byte column chunks per lane at a time.  Memory-bound.
-constexpr int kC = 4;
+// A wavefront sums kC 16-byte column chunks per lane of one token, in slot order in float32, the
+// loads of B rows in flight together.  Memory-bound; with few tokens kC = 1 spreads a token's columns
+// over wavefronts.  The token's rows come from the map (an entry counts only if it points inside
+// [0, L) at a row that names the pair, so stale entries are ignored), or, with kScan (few rows, k <=
+// 64), from a look through row_pair itself, which saves the launch that fills the map.
+constexpr int kScanRows = 1024;
 
-template <bool kBF16>
+template <bool kBF16, bool kScan, int kC, int B>
 __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restrict__ map,
                                                          const int32_t* __restrict__ row_pair,
                                                          const int32_t* __restrict__ fwd_off,
@@ -667,58 +874,122 @@ __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restri
                                                          const uint4* residual, uint4* out,
                                                          int32_t* __restrict__ err) {
   using C = Chunk<kBF16>;
-  const int lane = lane_id();
+  __shared__ int slots[kWavesPerBlock][kWave];
+  const int lane = lane_id(), w = threadIdx.x / kWave;
   const int L = clampi(fwd_off[E_loc], 0, L_cap);
+  const int parts = (hch + kC * kWave - 1) / (kC * kWave);
   const int64_t nw = (int64_t)gridDim.x * kWavesPerBlock;
-  for (int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + threadIdx.x / kWave; t < T; t += nw) {
-    for (int c0 = 0; c0 < hch; c0 += kC * kWave) {
-      float acc[kC][C::V];
+  for (int64_t id = (int64_t)blockIdx.x * kWavesPerBlock + w; id < (int64_t)T * parts; id += nw) {
+    const int64_t t = id / parts;
+    const int c0 = (int)(id - t * parts) * kC * kWave + lane;
+    float acc[kC][C::V];
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int ch = c0 + lane + c * kWave;
-        if (residual != nullptr && ch < hch)
-          C::get(load_nt(residual + t * hch + ch), acc[c]);
-        else
-          for (int q = 0; q < C::V; ++q) acc[c][q] = 0.0f;
+    for (int c = 0; c < kC; ++c) {
+      const int ch = c0 + c * kWave;
+      if (residual != nullptr && ch < hch)
+        C::get(load_nt(residual + t * hch + ch), acc[c]);
+      else
+        for (int q = 0; q < C::V; ++q) acc[c][q] = 0.0f;
+    }
+    if constexpr (kScan) {
+      slots[w][lane] = -1;
+      __builtin_amdgcn_wave_barrier();
+      bool bad = false;
+      for (int r = lane; r < L; r += kWave) {
+        const int p = row_pair[r], j = p - (int)t * k;
+        bad |= p < 0 || p >= (int64_t)T * k;
+        if (j >= 0 && j < k) bad |= atomicExch(&slots[w][j], r) != -1;   // two rows of one pair
       }
-      for (int j0 = 0; j0 < k; j0 += kWave) {
-        const int64_t p = t * k + j0 + lane;
-        int r = -1;
-        float a = 0.0f;
-        if (j0 + lane < k) {
+      if (bad) set_error(err, LRM_DEVERR_INDEX);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    for (int j0 = 0; j0 < k; j0 += kWave) {
+      const int64_t p = t * k + j0 + lane;
+      int r = -1;
+      float a = 0.0f;
+      if (j0 + lane < k) {
+        if constexpr (kScan) {
+          r = slots[w][lane];
+        } else {
           const int v = map[p];
-          if (v >= 0 && v < L && row_pair[v] == p) {
-            r = v;
-            a = topk_w[p];
-          }
+          if (v >= 0 && v < L && row_pair[v] == p) r = v;
         }
-        for (uint64_t m = ballot(r >= 0); m; m &= m - 1) {   // slots in ascending order
+        if (r >= 0) a = topk_w[p];
+      }
+      for (uint64_t m = ballot(r >= 0); m;) {   // slots in ascending order, B at a time
+        uint4 x[B][kC];
+        float wt[B];
+        int n = 0;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          if (m == 0) break;
           const int jj = __builtin_ctzll(m);
-          const uint4* src = y + (int64_t)__shfl(r, jj, kWave) * hch;
-          const float w = __shfl(a, jj, kWave);
+          m &= m - 1;
+          ++n;
+          const uint4* src = y + (int64_t)__builtin_amdgcn_readlane(r, jj) * hch;
+          wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), jj));
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
-            const int ch = c0 + lane + c * kWave;
-            float v[C::V];
-            C::get(ch < hch ? load_nt(src + ch) : make_uint4(0, 0, 0, 0), v);
+            const int ch = c0 + c * kWave;
+            x[b][c] = ch < hch ? load_nt(src + ch) : make_uint4(0, 0, 0, 0);
+          }
+        }
 #pragma unroll
-            for (int q = 0; q < C::V; ++q) acc[c][q] += w * v[q];
+        for (int b = 0; b < B; ++b) {
+          if (b >= n) break;
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            float v[C::V];
+            C::get(x[b][c], v);
+#pragma unroll
+            for (int q = 0; q < C::V; ++q) acc[c][q] += wt[b] * v[q];
           }
         }
       }
+    }
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int ch = c0 + lane + c * kWave;
-        if (ch < hch) out[t * hch + ch] = C::put(acc[c]);
-      }
+    for (int c = 0; c < kC; ++c) {
+      const int ch = c0 + c * kWave;
+      if (ch < hch) out[t * hch + ch] = C::put(acc[c]);
     }
   }
-  // every row must own its map entry; two rows that name one pair leave one of them unread
-  const int64_t n = (int64_t)gridDim.x * kBlock;
-  for (int64_t r = (int64_t)blockIdx.x * kBlock + threadIdx.x; r < L; r += n) {
-    const int p = row_pair[r];
-    if (p >= 0 && p < (int64_t)T * k && map[p] != r) set_error(err, LRM_DEVERR_INDEX);
+  if constexpr (!kScan) {
+    // every row must own its map entry; two rows that name one pair leave one of them unread
+    const int64_t n = (int64_t)gridDim.x * kBlock;
+    for (int64_t r = (int64_t)blockIdx.x * kBlock + threadIdx.x; r < L; r += n) {
+      const int p = row_pair[r];
+      if (p >= 0 && p < (int64_t)T * k && map[p] != r) set_error(err, LRM_DEVERR_INDEX);
+    }
   }
+}
+
+template <bool kBF16, bool kScan, int kC, int B>
+void launch_tokens(const lrm_problem& p, const int32_t* map, const int32_t* row_pair,
+                   const int32_t* fwd_off, const float* topk_w, const void* y, const void* residual,
+                   void* out, int32_t* err, hipStream_t s) {
+  const int hch = p.h * (kBF16 ? 2 : 4) / 16;
+  const int64_t waves = (int64_t)p.T * ((hch + kC * kWave - 1) / (kC * kWave));
+  const int64_t nb = (waves + kWavesPerBlock - 1) / kWavesPerBlock;
+  hipLaunchKernelGGL((combine_tokens<kBF16, kScan, kC, B>), dim3((unsigned)(nb < 16384 ? nb : 16384)),
+                     dim3(kBlock), 0, s, map, row_pair, fwd_off, p.E_loc, p.L_cap, p.T, p.k, topk_w,
+                     (const uint4*)y, hch, (const uint4*)residual, (uint4*)out, err);
+}
+
+template <bool kBF16>
+void launch_combine_t(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,
+                      const float* topk_w, const void* y, const void* residual, void* out, char* ws,
+                      hipStream_t s) {
+  int32_t* err = (int32_t*)ws;
+  int32_t* map = (int32_t*)(ws + kForwardMap);
+  if (p.L_cap <= kScanRows && p.k <= kWave) {
+    launch_tokens<kBF16, true, 1, 8>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
+    return;
+  }
+  const int64_t lb = ((int64_t)p.L_cap + kBlock - 1) / kBlock;
+  hipLaunchKernelGGL(forward_rows, dim3((unsigned)(lb < 2048 ? lb : 2048)), dim3(kBlock), 0, s,
+                     row_pair, fwd_off, p.E_loc, p.L_cap, (int64_t)p.T * p.k, map, err);
+  launch_tokens<kBF16, false, 4, 2>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
 }
 
 }  // namespace
@@ -741,22 +1012,10 @@ hipError_t launch_fc2(const lrm_problem& p, const int32_t* fwd_off, const void* 
 hipError_t launch_combine(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,
                           const float* topk_w, const void* y, const void* residual, void* out,
                           char* ws, hipStream_t s) {
-  int32_t* err = (int32_t*)ws;
-  int32_t* map = (int32_t*)(ws + kForwardMap);
-  const int64_t lb = ((int64_t)p.L_cap + kBlock - 1) / kBlock;
-  hipLaunchKernelGGL(forward_rows, dim3((unsigned)(lb < 2048 ? lb : 2048)), dim3(kBlock), 0, s,
-                     row_pair, fwd_off, p.E_loc, p.L_cap, (int64_t)p.T * p.k, map, err);
-  const int64_t tb = ((int64_t)p.T + kWavesPerBlock - 1) / kWavesPerBlock;
-  const unsigned nb = (unsigned)(tb < 16384 ? tb : 16384);
-  const int hch = p.h * (p.dtype == LRM_BF16 ? 2 : 4) / 16;
   if (p.dtype == LRM_BF16)
-    hipLaunchKernelGGL(combine_tokens<true>, dim3(nb), dim3(kBlock), 0, s, map, row_pair, fwd_off,
-                       p.E_loc, p.L_cap, p.T, p.k, topk_w, (const uint4*)y, hch,
-                       (const uint4*)residual, (uint4*)out, err);
+    launch_combine_t<true>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
   else
-    hipLaunchKernelGGL(combine_tokens<false>, dim3(nb), dim3(kBlock), 0, s, map, row_pair, fwd_off,
-                       p.E_loc, p.L_cap, p.T, p.k, topk_w, (const uint4*)y, hch,
-                       (const uint4*)residual, (uint4*)out, err);
+    launch_combine_t<false>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
   return hipGetLastError();
 }
 

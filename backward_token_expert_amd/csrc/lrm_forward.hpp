@@ -13,20 +13,22 @@ constexpr int kRouteBlocks = 256;
 struct RouteWs {
   size_t err;      // int32 error word of the last lrm_route
   size_t tokens;   // int32 [kRouteBlocks][2] valid tokens, error bits
-  size_t counts;   // int32 [kRouteBlocks][E] pairs per expert
-  size_t prob;     // float [kRouteBlocks][E] sums of probabilities
+  size_t counts;   // int32 [kRouteBlocks][pitch] pairs per expert
+  size_t prob;     // float [kRouteBlocks][pitch] sums of probabilities
   size_t total;
+  int pitch;       // E rounded up to 4
 };
 
 inline RouteWs route_ws(int E) {
   RouteWs w{};
+  w.pitch = (E + 3) / 4 * 4;
   size_t off = 256;
   w.tokens = off;
   off = align_up(off + (size_t)kRouteBlocks * 8, 256);
   w.counts = off;
-  off = align_up(off + (size_t)kRouteBlocks * E * 4, 256);
+  off = align_up(off + (size_t)kRouteBlocks * w.pitch * 4, 256);
   w.prob = off;
-  off = align_up(off + (size_t)kRouteBlocks * E * 4, 256);
+  off = align_up(off + (size_t)kRouteBlocks * w.pitch * 4, 256);
   w.total = off;
   return w;
 }

@@ -29,11 +29,21 @@ constexpr int kWavesPerBlock = kBlock / kWave;
 constexpr double kKeyInf = 0x1p200;
 constexpr double kNoKey = -0x1p300;   // below every key
 
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
 __device__ __forceinline__ double route_key(float v, int e) {
-  double d = (double)(v + 0.0f);
-  d = fmin(fmax(d, -kKeyInf), kKeyInf);
-  const int64_t b = __double_as_longlong(d);
-  return __longlong_as_double(b | (b < 0 ? e : 4095 - e));
+  const double d = min64(max64((double)(v + 0.0f), -kKeyInf), kKeyInf);   // NaN: the other operand
+  const int hi = __double2hiint(d);
+  return __hiloint2double(hi, __double2loint(d) | ((e ^ 4095) ^ ((hi >> 31) & 4095)));
 }
 
 __device__ __forceinline__ int key_expert(double k) {
@@ -76,8 +86,9 @@ struct RouteArgs {
   float* topk_w;
   float* lse;
   int32_t* part_tokens;  // [blocks][2]
-  int32_t* part_counts;  // [blocks][E]
-  float* part_prob;      // [blocks][E]
+  int pitch;             // E rounded up to 4
+  int32_t* part_counts;  // [blocks][pitch], columns past E are 0
+  float* part_prob;      // [blocks][pitch]
 };
 
 // One wavefront per token, any E and k: k rounds, each taking the largest key below the last one
@@ -156,15 +167,15 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void route_any(RouteArgs a) {
     sh_bad[w] = any_bad ? LRM_DEVERR_NONFINITE : 0;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kAnyWaves * kWave) {
+  for (int e = threadIdx.x; e < a.pitch; e += kAnyWaves * kWave) {
     float p = 0.0f;
     int c = 0;
-    for (int q = 0; q < kAnyWaves; ++q) {
+    for (int q = 0; q < kAnyWaves && e < E; ++q) {
       p += shared[q * E + e];
       c += ((int*)(shared + kAnyWaves * E))[q * E + e];
     }
-    a.part_prob[(int64_t)blockIdx.x * E + e] = p;
-    a.part_counts[(int64_t)blockIdx.x * E + e] = c;
+    a.part_prob[(int64_t)blockIdx.x * a.pitch + e] = p;
+    a.part_counts[(int64_t)blockIdx.x * a.pitch + e] = c;
   }
   if (threadIdx.x == 0) {
     int n = 0, b = 0;
@@ -179,23 +190,13 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void route_any(RouteArgs a) {
 
 // Registers-only routing for k <= KT and E <= LPT * VPL: LPT adjacent lanes share a token, each
 // holding up to VPL logits in 16-byte chunks (chunk i * LPT + sub, so a token's lanes read 16 LPT
-// consecutive bytes).  Each lane keeps its KT largest keys sorted by inserting every key (one
-// maximum and one minimum per place, both single float64 instructions: the insertion costs 2 KT
-// instructions a logit where a compare and four selects would cost 5 KT), then log2(LPT) merges
-// of two sorted lists (maximum of one list against the other reversed, then a bitonic sort) leave
-// the token's list in all its lanes.  Few lanes a token keep the wave's work in the insertions of
-// distinct logits rather than in reductions that every lane repeats.
-__device__ __forceinline__ double max64(double a, double b) {
-  double r;
-  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-  return r;
-}
-__device__ __forceinline__ double min64(double a, double b) {
-  double r;
-  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-  return r;
-}
-
+// consecutive bytes).  Each lane sorts its keys in groups of KT (an odd-even merge network; a
+// comparator is one float64 maximum and one minimum) and merges every group into the KT largest so
+// far (maximum of one list against the other reversed, then a bitonic sort); log2(LPT) merges
+// across lanes leave the token's list in all of them.  For KT = 8 that is 9 instructions a logit,
+// where inserting each key into the list takes 16, and the comparators of a stage do not wait for
+// each other.  Few lanes a token keep the wave's work in the sorting of distinct logits rather
+// than in the merges that every lane repeats.
 // The value of a lane of the other half of each group of 2 * O lanes (all lanes of a half hold the
 // same value when O > 1 and O < 16, so a mirror serves as the exchange).
 template <int O>
@@ -227,24 +228,48 @@ __device__ __forceinline__ float token_max(float v) {
   return v;
 }
 
+// Descending sort of N keys in registers: Batcher's odd-even merge network.
+template <int N>
+__device__ __forceinline__ void sort_keys(double (&t)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const double a = t[i + j], b = t[i + j + k];
+            t[i + j] = max64(a, b);
+            t[i + j + k] = min64(a, b);
+          }
+}
+
+// t, sorted, becomes the N largest of t and the sorted list whose reverse is r.
+template <int N>
+__device__ __forceinline__ void merge_keys(double (&t)[N], const double (&r)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) t[j] = max64(t[j], r[j]);
+#pragma unroll
+  for (int s = N / 2; s >= 1; s /= 2)
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (!(j & s)) {
+        const double a = t[j], b = t[j + s];
+        t[j] = max64(a, b);
+        t[j + s] = min64(a, b);
+      }
+}
+
 template <int KT, int LPT, int O = 1>
-__device__ __forceinline__ void merge_lists(double (&t)[KT]) {
+__device__ __forceinline__ void merge_lanes(double (&t)[KT]) {
   if constexpr (O < LPT) {
-    double u[KT];
+    double r[KT];
 #pragma unroll
-    for (int j = 0; j < KT; ++j) u[j] = max64(t[j], swap_half<O>(t[KT - 1 - j]));
-#pragma unroll
-    for (int s = KT / 2; s >= 1; s /= 2)
-#pragma unroll
-      for (int j = 0; j < KT; ++j)
-        if (!(j & s)) {
-          const double a = u[j], b = u[j + s];
-          u[j] = max64(a, b);
-          u[j + s] = min64(a, b);
-        }
-#pragma unroll
-    for (int j = 0; j < KT; ++j) t[j] = u[j];
-    merge_lists<KT, LPT, 2 * O>(t);
+    for (int j = 0; j < KT; ++j) r[j] = swap_half<O>(t[KT - 1 - j]);
+    merge_keys(t, r);
+    merge_lanes<KT, LPT, 2 * O>(t);
   }
 }
 
@@ -322,21 +347,26 @@ __global__ __launch_bounds__(WAVES * kWave) void route_rows(RouteArgs a, RouteOu
                               want, vec, v);
     double key[KT];
 #pragma unroll
-    for (int j = 0; j < KT; ++j) key[j] = kNoKey;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (i / CV * LPT * CV >= E) continue;   // uniform
-      const int e = (i / CV * LPT + sub) * CV + i % CV;
-      if (bad_logit(v[i])) bad = LRM_DEVERR_NONFINITE;
-      double x = e < E ? route_key(v[i], e) : kNoKey;
+    for (int i0 = 0; i0 < VPL; i0 += KT) {
+      if (i0 / CV * LPT * CV >= E) continue;   // uniform
+      double group[KT];
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
-        const double hi = max64(key[j], x);
-        x = min64(key[j], x);
-        key[j] = hi;
+        const int i = i0 + j, e = (i / CV * LPT + sub) * CV + i % CV;
+        group[j] = e < E ? route_key(v[i], e) : kNoKey;
+      }
+      sort_keys(group);
+      if (i0 == 0) {
+#pragma unroll
+        for (int j = 0; j < KT; ++j) key[j] = group[j];
+      } else {
+        double r[KT];
+#pragma unroll
+        for (int j = 0; j < KT; ++j) r[j] = group[KT - 1 - j];
+        merge_keys(key, r);
       }
     }
-    merge_lists<KT, LPT>(key);
+    merge_lanes<KT, LPT>(key);
     const float top = key_logit(key[0]);
     const bool ok = want && top > -INFINITY;
     const float m = ok ? top : 0.0f;
@@ -348,6 +378,7 @@ __global__ __launch_bounds__(WAVES * kWave) void route_rows(RouteArgs a, RouteOu
       sum += v[i];
     }
     sum = token_sum<LPT>(sum);
+    if (!(sum < INFINITY)) bad = LRM_DEVERR_NONFINITE;   // a NaN, or infinity less itself
     const float inv = ok ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -395,13 +426,15 @@ __global__ __launch_bounds__(WAVES * kWave) void route_rows(RouteArgs a, RouteOu
   __syncthreads();
   const int n = live_sum;
   double mine = 0.0;   // of sum_e counts[e] * (sum of p_te), where this workgroup is the only one
-  for (int e = threadIdx.x; e < E; e += THREADS) {
+  for (int e = threadIdx.x; e < (gridDim.x > 1 ? a.pitch : E); e += THREADS) {
     float x = 0.0f;
-#pragma unroll 4
-    for (int q = 0; q < WAVES * ROWS; ++q) x += part[q * E + e];
+    if (e < E) {
+#pragma unroll 8
+      for (int q = 0; q < WAVES * ROWS; ++q) x += part[q * E + e];
+    }
     if (gridDim.x > 1) {
-      a.part_prob[(int64_t)blockIdx.x * E + e] = x;
-      a.part_counts[(int64_t)blockIdx.x * E + e] = counts[e];
+      a.part_prob[(int64_t)blockIdx.x * a.pitch + e] = x;
+      a.part_counts[(int64_t)blockIdx.x * a.pitch + e] = e < E ? counts[e] : 0;
     } else {
       o.counts[e] = counts[e];
       o.prob[e] = n > 0 ? (float)((double)x / n) : 0.0f;
@@ -428,67 +461,90 @@ __global__ __launch_bounds__(WAVES * kWave) void route_rows(RouteArgs a, RouteOu
   }
 }
 
-// Sums the workgroups' partial results: counts, prob, the loss and the error word.  One workgroup
-// of 1024 threads; thread (slice, e) adds every S-th workgroup's row in float64, then slice 0 adds
-// the slices.
-constexpr int kFinalThreads = 1024;
+// Sums the workgroups' partial results: counts, prob, the loss and the error word.  One workgroup;
+// thread (slice, q) adds four experts' columns of every S-th workgroup's row in float64, kBatch rows
+// in flight (one after the other the rows' latencies were all of this kernel's time: 17 us for 256
+// rows of 128 experts), then the slices are added in order.
+constexpr int kFinalThreads = 1024, kBatch = 8;
 
 __global__ __launch_bounds__(kFinalThreads) void route_final(const int32_t* __restrict__ part_tokens,
                                                              const int32_t* __restrict__ part_counts,
                                                              const float* __restrict__ part_prob,
-                                                             int blocks, int E, int k, float coef,
-                                                             int32_t* __restrict__ counts,
+                                                             int blocks, int E, int pitch, int k,
+                                                             float coef, int32_t* __restrict__ counts,
                                                              float* __restrict__ prob,
                                                              float* __restrict__ loss,
                                                              int32_t* __restrict__ err) {
-  __shared__ double sp[kFinalThreads];
-  __shared__ int sc[kFinalThreads];
+  __shared__ double sp[kFinalThreads][4];
+  __shared__ int sc[kFinalThreads][4];
+  __shared__ double sums[kFinalThreads / kWave];
   __shared__ int tokens, bits;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, Q = pitch / 4, S = kFinalThreads / Q;   // pitch <= 4096
+  const int slice = tid / Q, q = tid % Q;
   if (tid == 0) tokens = bits = 0;
-  __syncthreads();
-  for (int b = tid; b < blocks; b += kFinalThreads) {
-    atomicAdd(&tokens, part_tokens[2 * b]);
-    atomicOr(&bits, part_tokens[2 * b + 1]);
-  }
-  __syncthreads();
-  const int n = tokens;
-  const int width = E >= kFinalThreads ? kFinalThreads : (E + kWave - 1) / kWave * kWave;
-  const int S = kFinalThreads / width;
-  const int slice = tid / width;
-  double sum = 0.0;   // sum_e counts[e] * (sum of p_te)
-  for (int e0 = 0; e0 < E; e0 += width) {
-    const int e = e0 + tid % width;
-    double p = 0.0;
-    int c = 0;
-    if (e < E && slice < S)
-      for (int b = slice; b < blocks; b += S) {
-        p += part_prob[(int64_t)b * E + e];
-        c += part_counts[(int64_t)b * E + e];
+  double p[4] = {0.0, 0.0, 0.0, 0.0};
+  int c[4] = {0, 0, 0, 0};
+  if (slice < S)
+    for (int b0 = slice; b0 < blocks; b0 += kBatch * S) {
+      float4 x[kBatch];
+      int4 y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int b = b0 + i * S;
+        x[i] = b < blocks ? ((const float4*)(part_prob + (int64_t)b * pitch))[q] : make_float4(0, 0, 0, 0);
+        y[i] = b < blocks ? ((const int4*)(part_counts + (int64_t)b * pitch))[q] : make_int4(0, 0, 0, 0);
       }
-    sp[tid] = p;
-    sc[tid] = c;
-    __syncthreads();
-    if (slice == 0 && e < E) {
-      for (int q = 1; q < S; ++q) {
-        p += sp[tid + q * width];
-        c += sc[tid + q * width];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        p[0] += x[i].x;
+        p[1] += x[i].y;
+        p[2] += x[i].z;
+        p[3] += x[i].w;
+        c[0] += y[i].x;
+        c[1] += y[i].y;
+        c[2] += y[i].z;
+        c[3] += y[i].w;
       }
-      counts[e] = c;
-      prob[e] = n > 0 ? (float)(p / n) : 0.0f;
-      sum += p * c;
     }
-    __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sp[tid][i] = p[i];
+    sc[tid][i] = c[i];
   }
-  sp[tid] = sum;
   __syncthreads();
-  for (int o = kFinalThreads / 2; o >= 1; o >>= 1) {
-    if (tid < o) sp[tid] += sp[tid + o];
-    __syncthreads();
+  int n = 0, bad = 0;
+  for (int b = tid; b < blocks; b += kFinalThreads) {
+    n += part_tokens[2 * b];
+    bad |= part_tokens[2 * b + 1];
   }
+  n = wave_sum_int(n);
+  bad = ballot(bad != 0) != 0 ? LRM_DEVERR_NONFINITE : 0;
+  if (lane_id() == 0) {
+    atomicAdd(&tokens, n);
+    atomicOr(&bits, bad);
+  }
+  __syncthreads();
+  n = tokens;
+  double sum = 0.0;   // sum_e counts[e] * (sum of p_te)
+  for (int e = tid; e < E; e += kFinalThreads) {
+    double x = 0.0;
+    int y = 0;
+    for (int i = 0; i < S; ++i) {
+      x += sp[i * Q + e / 4][e % 4];
+      y += sc[i * Q + e / 4][e % 4];
+    }
+    counts[e] = y;
+    prob[e] = n > 0 ? (float)(x / n) : 0.0f;
+    sum += x * y;
+  }
+  sum = wave_sum(sum);
+  if (lane_id() == 0) sums[tid / kWave] = sum;
+  __syncthreads();
   if (tid == 0) {
+    double x = 0.0;
+    for (int i = 0; i < kFinalThreads / kWave; ++i) x += sums[i];
     const double nn = n;
-    *loss = n > 0 ? (float)((double)coef * E * sp[0] / (nn * nn * k)) : 0.0f;
+    *loss = n > 0 ? (float)((double)coef * E * x / (nn * nn * k)) : 0.0f;
     *err = bits;
   }
 }
@@ -506,41 +562,68 @@ __global__ __launch_bounds__(WAVES * kWave) void route_backward(const void* __re
                                                                 float coef, int vec,
                                                                 float* __restrict__ dlogits) {
   constexpr int CV = kBF16 ? 8 : 4, TPW = kWave / LPT;
+  constexpr int G = LPT >= 8 ? 1 : 8 / LPT;   // choices a lane has in registers
   extern __shared__ float shared[];
   const int lane = lane_id(), w = threadIdx.x / kWave, sub = lane % LPT;
   float* extra = shared + (w * TPW + lane / LPT) * E;   // this token's row
   int pairs = 0;
   for (int e = lane; e < E; e += kWave) pairs += counts[e];
-  pairs = wave_sum_int(pairs);
-  // f_e = counts[e] / (n k) and c = coef E / n with n = pairs / k
-  const float f1 = pairs > 0 ? 1.0f / (float)pairs : 0.0f;
-  const float c = pairs > 0 ? (float)((double)coef * E * k / pairs) : 0.0f;
-  float f[VPL];
+  int n[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = (i / CV * LPT + sub) * CV + i % CV;
-    f[i] = e < E ? f1 * counts[e] : 0.0f;
+    n[i] = e < E ? counts[e] : 0;
     if (adot != nullptr && e < E) extra[e] = 0.0f;
   }
+  float f[VPL], c = 0.0f;
+  bool first = true;
   const bool vec_out = E % 4 == 0;
   const int64_t step = (int64_t)gridDim.x * WAVES * TPW;
   for (int64_t t0 = ((int64_t)blockIdx.x * WAVES + w) * TPW; t0 < T; t0 += step) {
     const int64_t t = t0 + lane / LPT;
-    const bool in = t < T, ok = in && topk_idx[t * k] >= 0;
+    const bool in = t < T;
+    // every load of the token at once: the row (also of a token that turns out not to be valid), its
+    // choices and their terms
     float v[VPL];
-    load_row<kBF16, LPT, VPL>((const char*)logits + (ok ? t : 0) * E * (kBF16 ? 2 : 4), E, sub, ok,
-                              vec, v);
+    load_row<kBF16, LPT, VPL>((const char*)logits + (in ? t : 0) * E * (kBF16 ? 2 : 4), E, sub, in, vec, v);
+    int ge[G];
+    float ga[G], gw[G];
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      const int j = sub + q * LPT;
+      const bool has = in && adot != nullptr && j < k;
+      ge[q] = has ? topk_idx[t * k + j] : -1;
+      ga[q] = has ? adot[t * k + j] : 0.0f;
+      gw[q] = has && gate == LRM_GATE_TOPK ? topk_w[t * k + j] : 0.0f;
+    }
+    const bool ok = in && topk_idx[t * k] >= 0;
+    if (first) {
+      // f_e = counts[e] / (n k) and c = coef E / n with n = pairs / k
+      pairs = wave_sum_int(pairs);
+      const float f1 = pairs > 0 ? 1.0f / (float)pairs : 0.0f;
+      c = pairs > 0 ? (float)((double)coef * E * k / pairs) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) f[i] = f1 * n[i];
+      first = false;
+    }
     float S = 0.0f;
     if (adot != nullptr) {
-      if (ok)
-        for (int j = sub; j < k; j += LPT) S += adot[t * k + j];
+#pragma unroll
+      for (int q = 0; q < G; ++q) S += ga[q];
+      if (in)
+        for (int j = sub + G * LPT; j < k; j += LPT) S += adot[t * k + j];
       S = token_sum<LPT>(S);
-      if (ok)
-        for (int j = sub; j < k; j += LPT) {
+      S = ok ? S : 0.0f;
+      if (ok) {
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+          if (ge[q] >= 0 && ge[q] < E) atomicAdd(&extra[ge[q]], ga[q] - gw[q] * S);
+        for (int j = sub + G * LPT; j < k; j += LPT) {
           const int e = topk_idx[t * k + j];
           const float x = adot[t * k + j] - (gate == LRM_GATE_TOPK ? topk_w[t * k + j] * S : 0.0f);
           if (e >= 0 && e < E) atomicAdd(&extra[e], x);
         }
+      }
     }
     float m = -INFINITY;
 #pragma unroll
@@ -571,7 +654,7 @@ __global__ __launch_bounds__(WAVES * kWave) void route_backward(const void* __re
         float g[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          g[q] = v[4 * i + q] * inv * (c * (f[4 * i + q] - fp) - all);
+          g[q] = ok ? v[4 * i + q] * inv * (c * (f[4 * i + q] - fp) - all) : 0.0f;
           if (adot != nullptr && e0 + q < E) g[q] += extra[e0 + q];
         }
         float* out = dlogits + t * E + e0;
@@ -586,11 +669,15 @@ __global__ __launch_bounds__(WAVES * kWave) void route_backward(const void* __re
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (adot != nullptr && ok)
-      for (int j = sub; j < k; j += LPT) {
+    if (adot != nullptr && ok) {
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+        if (ge[q] >= 0 && ge[q] < E) extra[ge[q]] = 0.0f;
+      for (int j = sub + G * LPT; j < k; j += LPT) {
         const int e = topk_idx[t * k + j];
         if (e >= 0 && e < E) extra[e] = 0.0f;
       }
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
@@ -745,13 +832,14 @@ hipError_t launch_route(const lrm_router& r, const void* logits, const uint8_t* 
                         float* loss, char* ws, hipStream_t s) {
   const RouteWs wl = route_ws(r.E);
   const RouteArgs a{logits, mask, r.T, r.E, r.k, r.gate, topk_idx, topk_w, lse,
-                    (int32_t*)(ws + wl.tokens), (int32_t*)(ws + wl.counts), (float*)(ws + wl.prob)};
+                    (int32_t*)(ws + wl.tokens), wl.pitch, (int32_t*)(ws + wl.counts),
+                    (float*)(ws + wl.prob)};
   const RouteOut o{counts, prob, loss, (int32_t*)(ws + wl.err), r.balance_coef};
   const unsigned nb = r.dtype == LRM_BF16 ? launch_rows_any<true>(a, o, s) : launch_rows_any<false>(a, o, s);
   // route_rows of one workgroup ends with the results themselves: one launch for a short batch
   if (nb > 1 || r.k > 16)
     hipLaunchKernelGGL(route_final, dim3(1), dim3(kFinalThreads), 0, s, a.part_tokens, a.part_counts,
-                       a.part_prob, (int)nb, r.E, r.k, r.balance_coef, counts, prob, loss,
+                       a.part_prob, (int)nb, r.E, wl.pitch, r.k, r.balance_coef, counts, prob, loss,
                        (int32_t*)(ws + wl.err));
   return hipGetLastError();
 }

@@ -331,18 +331,32 @@ _F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
 
 def _arg(t, name, types, count, device, exact=False):
     """The address of tensor ``t`` of at least (or exactly) ``count`` elements, after its checks."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
+    n = t.numel()
+    if t.dtype in types and (n == count or n > count and not exact) and t.is_contiguous() and \
+            t.get_device() == device:
+        return t.data_ptr()
     if t.dtype not in types:
         raise LrmError(f"{name}: element type {t.dtype}, expected {types[0]}")
-    n = t.numel()
     if n < count or (exact and n != count):
         raise LrmError(f"{name}: {n} elements, expected {'' if exact else 'at least '}{count}")
     if not t.is_contiguous():
         raise LrmError(f"{name}: not contiguous")
-    if t.device.type != "cuda" or t.device.index != device:
-        raise LrmError(f"{name}: on {t.device}, the call runs on cuda:{device}")
-    return t.data_ptr()
+    raise LrmError(f"{name}: on {t.device}, the call runs on cuda:{device}")
+
+
+# The handle of torch's current stream.  A call of a serving step is a few microseconds of host time;
+# forming a Stream object for its handle would be three more.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _queue(stream, device):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+        raise LrmError(f"stream: on cuda:{stream.device_index}, the call runs on cuda:{device}")
+    return _stream(stream)
 
 
 def _device() -> int:
@@ -386,7 +400,7 @@ def lrm_route(router, logits, mask, topk_idx, topk_w, lse, counts, prob, loss, w
                               _arg(topk_w, "topk_w", _F32, r.T * r.k, d),
                               _arg(lse, "lse", _F32, r.T, d), _arg(counts, "counts", _I32, r.E, d),
                               _arg(prob, "prob", _F32, r.E, d), _arg(loss, "loss", _F32, 1, d),
-                              *_space(ws, d), _stream(stream)), "lrm_route")
+                              *_space(ws, d), _queue(stream, d)), "lrm_route")
 
 
 def lrm_route_backward(router, logits, topk_idx, topk_w, counts, adot, dlogits, stream=None):
@@ -397,7 +411,7 @@ def lrm_route_backward(router, logits, topk_idx, topk_w, counts, adot, dlogits, 
         _arg(topk_idx, "topk_idx", _I32, r.T * r.k, d), _arg(topk_w, "topk_w", _F32, r.T * r.k, d),
         _arg(counts, "counts", _I32, r.E, d),
         _arg(adot, "adot", _F32, r.T * r.k, d), _arg(dlogits, "dlogits", _F32, r.T * r.E, d),
-        _stream(stream)), "lrm_route_backward")
+        _queue(stream, d)), "lrm_route_backward")
 
 
 def lrm_gate_dots(problem, sel_pair, cmp_off, dphi, Phic, adot, ws, stream=None):
@@ -407,7 +421,7 @@ def lrm_gate_dots(problem, sel_pair, cmp_off, dphi, Phic, adot, ws, stream=None)
         ctypes.byref(p), _arg(sel_pair, "sel_pair", _I32, p.K_cap, d),
         _arg(cmp_off, "cmp_off", _I32, p.E_loc + 1, d), _arg(dphi, "dphi", _F32, p.K_cap * p.d, d),
         _arg(Phic, "Phic", _elem(p.dtype), p.K_cap * p.d, d), _arg(adot, "adot", _F32, p.T * p.k, d),
-        *_space(ws, d), _stream(stream)), "lrm_gate_dots")
+        *_space(ws, d), _queue(stream, d)), "lrm_gate_dots")
 
 
 def lrm_grouped_fc1_swiglu(problem, row_pair, fwd_off, x, W1, ac, phi, ws, stream=None):
@@ -419,7 +433,7 @@ def lrm_grouped_fc1_swiglu(problem, row_pair, fwd_off, x, W1, ac, phi, ws, strea
         ctypes.byref(p), _arg(row_pair, "row_pair", _I32, p.L_cap, d),
         _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d), _arg(x, "x", el, p.T * p.h, d),
         _arg(W1, "W1", el, p.E_loc * 2 * p.d * p.h, d), _arg(ac, "ac", el, p.L_cap * 2 * p.d, d),
-        _arg(phi, "phi", el, p.L_cap * p.d, d), *_space(ws, d), _stream(stream)),
+        _arg(phi, "phi", el, p.L_cap * p.d, d), *_space(ws, d), _queue(stream, d)),
         "lrm_grouped_fc1_swiglu")
 
 
@@ -430,7 +444,7 @@ def lrm_grouped_fc2(problem, fwd_off, phi, W, y, ws, stream=None):
     _check(lib, lib.lrm_grouped_fc2(
         ctypes.byref(p), _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d),
         _arg(phi, "phi", el, p.L_cap * p.d, d), _arg(W, "W", el, p.E_loc * p.h * p.d, d),
-        _arg(y, "y", el, p.L_cap * p.h, d), *_space(ws, d), _stream(stream)), "lrm_grouped_fc2")
+        _arg(y, "y", el, p.L_cap * p.h, d), *_space(ws, d), _queue(stream, d)), "lrm_grouped_fc2")
 
 
 def lrm_combine_tokens(problem, row_pair, fwd_off, topk_w, y, residual, out, ws, stream=None):
@@ -442,7 +456,7 @@ def lrm_combine_tokens(problem, row_pair, fwd_off, topk_w, y, residual, out, ws,
         ctypes.byref(p), _arg(row_pair, "row_pair", _I32, p.L_cap, d),
         _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d), _arg(topk_w, "topk_w", _F32, p.T * p.k, d),
         _arg(y, "y", el, p.L_cap * p.h, d), _arg(residual, "residual", el, p.T * p.h, d),
-        _arg(out, "out", el, p.T * p.h, d), *_space(ws, d), _stream(stream)), "lrm_combine_tokens")
+        _arg(out, "out", el, p.T * p.h, d), *_space(ws, d), _queue(stream, d)), "lrm_combine_tokens")
 
 
 class TensorList:
@@ -492,14 +506,14 @@ def lrm_grad_norm(tensors, norm, ws, stream=None):
     lib = load_library()
     d = _on_device(tensors)
     _check(lib, lib.lrm_grad_norm(tensors.array, tensors.n, _arg(norm, "norm", _F32, 1, d),
-                                  *_space(ws, d), _stream(stream)), "lrm_grad_norm")
+                                  *_space(ws, d), _queue(stream, d)), "lrm_grad_norm")
 
 
 def lrm_clip_grads(tensors, max_norm, norm, ws, stream=None):
     lib = load_library()
     d = _on_device(tensors)
     _check(lib, lib.lrm_clip_grads(tensors.array, tensors.n, max_norm, _arg(norm, "norm", _F32, 1, d),
-                                   *_space(ws, d), _stream(stream)), "lrm_clip_grads")
+                                   *_space(ws, d), _queue(stream, d)), "lrm_clip_grads")
 
 
 def lrm_read_device_error(ws, clear: bool = False, stream=None) -> int:
