@@ -439,8 +439,9 @@ lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, c
   LRM_TRY(check_problem(problem));
   if (!fwd_off || !phi || !W || !y) return LRM_ERR_INVALID_ARGUMENT;
   if (!aligned16(phi) || !aligned16(W) || !aligned16(y)) return LRM_ERR_UNSUPPORTED;
-  if ((int64_t)problem->h * problem->d * element_bytes(problem->dtype) > kMaxOperand)
-    return LRM_ERR_UNSUPPORTED;
+  // one expert's weights, and the 256 rows of phi of a tile
+  const int64_t row = problem->d * element_bytes(problem->dtype);
+  if (problem->h * row > kMaxOperand || 256 * row > kMaxOperand) return LRM_ERR_UNSUPPORTED;
   LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
   return from_hip(lrm::launch_fc2(*problem, fwd_off, phi, W, y, stream));
 }

@@ -6,7 +6,6 @@
 // whose backward the other calls compute).  Both products contract over the contiguous axis of
 // both operands (rows of x or phi against rows of W1 or W).
 #include <math.h>
-#include <stdlib.h>
 
 #include "lrm_device.hpp"
 #include "lrm_forward.hpp"
@@ -23,34 +22,42 @@ constexpr int kWavesPerBlock = kBlock / kWave;
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
 // Row tile `idx` of the experts' segments cut into tiles of BM rows: expert and row range.  e = -1
-// past the last one.  Every wave finds it by itself with one scan over 64 experts at a time, so no
-// launch builds a table of tiles.
+// past the last one.  Every wave finds it by itself with a scan over 64 experts at a time, the
+// offsets of 256 in flight, so no launch builds a table of tiles.
 struct RowTile {
   int e, r0, r1;
 };
 
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ fwd_off, int E_loc, int cap,
-                                             int idx) {
+                                             int64_t idx) {
+  constexpr int B = 4;
   const int lane = lane_id();
-  int base = 0;
-  for (int e0 = 0; e0 < E_loc; e0 += kWave) {
-    const int e = e0 + lane;
-    int a = 0, b = 0;
-    if (e < E_loc) {
-      a = clampi(fwd_off[e], 0, cap);
-      b = clampi(fwd_off[e + 1], a, cap);
+  int64_t base = 0;
+  for (int e0 = 0; e0 < E_loc; e0 += B * kWave) {
+    int a[B], b[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int e = e0 + i * kWave + lane;
+      a[i] = e < E_loc ? fwd_off[e] : 0;
+      b[i] = e < E_loc ? fwd_off[e + 1] : 0;
     }
-    const int n = (b - a + BM - 1) / BM;
-    const int inc = wave_inclusive_scan(n);
-    const uint64_t m = ballot(base + inc > idx);
-    if (m) {
-      const int l = __builtin_ctzll(m);
-      const int r0 = __shfl(a + (idx - (base + inc - n)) * BM, l, kWave);
-      const int end = __shfl(b, l, kWave);
-      return {e0 + l, r0, r0 + BM < end ? r0 + BM : end};
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (e0 + i * kWave >= E_loc) break;
+      a[i] = clampi(a[i], 0, cap);
+      b[i] = clampi(b[i], a[i], cap);
+      const int n = (b[i] - a[i] + BM - 1) / BM;
+      const int inc = wave_inclusive_scan(n);
+      const uint64_t m = ballot(base + inc > idx);
+      if (m) {
+        const int l = __builtin_ctzll(m);
+        const int r0 = __builtin_amdgcn_readlane(a[i] + (int)(idx - (base + inc - n)) * BM, l);
+        const int end = __builtin_amdgcn_readlane(b[i], l);
+        return {e0 + i * kWave + l, r0, r0 + BM < end ? r0 + BM : end};
+      }
+      base += __builtin_amdgcn_readlane(inc, kWave - 1);
     }
-    base += __shfl(inc, kWave - 1, kWave);
   }
   return {-1, 0, 0};
 }
@@ -78,113 +85,148 @@ struct FcArgs {
   void* out;
   void* out2;
   int32_t* err;
+  int64_t units;   // the most units (row tile, column tile) there can be
 };
 
-// 64 rows x 128 columns (for kSwiglu 64 of each half) by 4 wavefronts, each one 32 rows x two
-// 32-wide column tiles, which for kSwiglu are the same columns of the gate and the up half.
-constexpr int kBM = 64, kBNH = 64, kKS = 32;
+// The token of pair p, or -1 for a pair id that is none.
+__device__ __forceinline__ int64_t token_of(const FcArgs& g, int p) {
+  return p >= 0 && p < g.P ? p / g.k : -1;
+}
 
-template <bool kBF16, bool kSwiglu>
-__global__ __launch_bounds__(kBlock) void fc_tile(FcArgs g) {
-  constexpr int ESZ = kBF16 ? 2 : 4, V = 16 / ESZ, CH = kKS / V;  // elements, chunks per 16 bytes, row
-  constexpr int PITCH = kBF16 ? kKS + 8 : kKS + 4;
-  __shared__ __attribute__((aligned(16))) char sa[kBM * PITCH * ESZ];
-  __shared__ __attribute__((aligned(16))) char sb[2 * kBNH * PITCH * ESZ];
+// Operands are read through buffer resources: a row or chunk that is not there gets an offset beyond
+// the range and reads as zeros.
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+// Buffer resource of 2^31 bytes from base: every offset that is used lies below what the host checked.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
+  const uint64_t v = (uint64_t)(uintptr_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), (short)0,
+                                           (int)kOutOfRange, 0x00020000);
+}
+
+// ------------------------------------------------------------------------------------------------
+// float32 products: 64 rows x 64 columns (for kSwiglu 32 of each half) by 2 wavefronts, each one 32
+// rows x two 32-wide column tiles, which for kSwiglu are the same columns of the gate and the up
+// half.  Bound by the float32 matrix rate (64 cycles an MFMA, against one 16-byte LDS read a lane
+// for four of them): the next K step's loads are in registers while one is multiplied, and the
+// workgroups of a CU (eight, small ones, so that the last round of a small layer is short) cover
+// each other's barriers.  A lane's 16 bytes hold four k of one row; the i-th
+// MFMA takes the i-th of both operands, so k = 8 s + i and 8 s + 4 + i meet, in any order.
+// Rows of 128 k are summed apart and then added, which keeps the error of a long row's sum near
+// that of a short one's.
+// ------------------------------------------------------------------------------------------------
+constexpr int kBM = 64, kBNH = 32, kKS = 16, kPitch = kKS + 4, kRun = 128, kF32Threads = 128;
+
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+template <bool kSwiglu>
+__global__ __launch_bounds__(kF32Threads, 4) void fc_f32(FcArgs g) {
+  constexpr int CH = kKS / 4;
+  constexpr int NA = kBM * CH / kF32Threads, NB = 2 * kBNH * CH / kF32Threads;   // chunks a thread moves
+  __shared__ __attribute__((aligned(16))) float sa[kBM * kPitch];
+  __shared__ __attribute__((aligned(16))) float sb[2 * kBNH * kPitch];
   const int cols = (g.N + (kSwiglu ? kBNH : 2 * kBNH) - 1) / (kSwiglu ? kBNH : 2 * kBNH);
-  for (int64_t u = blockIdx.x;; u += gridDim.x) {   // unit = (row tile, column tile)
-  const RowTile t = find_tile<kBM>(g.fwd_off, g.E_loc, g.cap, (int)(u / cols));
-  if (t.e < 0) return;
-  const int n0 = (int)(u % cols) * (kSwiglu ? kBNH : 2 * kBNH);
-  const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave, wm = w >> 1, wn = w & 1;
-  const int64_t K = g.K;
-  const char* We = (const char*)g.B + (int64_t)t.e * (kSwiglu ? 2 : 1) * g.N * K * ESZ;
-  // this thread's chunks of A (one or two rows) and B
-  constexpr int NA = kBM * CH / kBlock, NB = 2 * kBNH * CH / kBlock;
-  const char* pa[NA];
-  const char* pb[NB];
-#pragma unroll
-  for (int j = 0; j < NA; ++j) {
-    const int q = tid + j * kBlock, r = t.r0 + q / CH;
-    int64_t src = -1;
-    if (r < t.r1) {
-      src = r;
-      if (kSwiglu) {
-        const int p = g.row_pair[r];
-        src = p >= 0 && p < g.P ? p / g.k : -1;
-        if (src < 0) set_error(g.err, LRM_DEVERR_INDEX);
-      }
-    }
-    pa[j] = src < 0 ? nullptr : (const char*)g.A + (src * K + (q % CH) * V) * ESZ;
-  }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int q = tid + j * kBlock, r = q / CH;   // row of the B tile
-    const int col = n0 + (kSwiglu ? r % kBNH : r);
-    pb[j] = col < g.N ? We + ((int64_t)(col + (kSwiglu ? r / kBNH * g.N : 0)) * K + (q % CH) * V) * ESZ : nullptr;
-  }
-  f32x16 acc[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[j][i] = 0.0f;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = 0; k0 < g.K; k0 += kKS) {
+  const int tid = threadIdx.x, lane = lane_id(), wm = tid / kWave;
+  const int kc = (tid % CH) * 4;   // this thread's k of a step
+  for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {   // unit = (row tile, column tile)
+    const RowTile t = find_tile<kBM>(g.fwd_off, g.E_loc, g.cap, u / cols);
+    if (t.e < 0) return;
+    const int n0 = (int)(u % cols) * (kSwiglu ? kBNH : 2 * kBNH);
+    const __amdgpu_buffer_rsrc_t ra = operand((const char*)g.A + (kSwiglu ? 0 : (int64_t)t.r0 * g.K * 4));
+    const __amdgpu_buffer_rsrc_t rb =
+        operand((const char*)g.B + (int64_t)t.e * (kSwiglu ? 2 : 1) * g.N * g.K * 4);
+    uint32_t oa[NA], ob[NB];
 #pragma unroll
     for (int j = 0; j < NA; ++j) {
-      const int q = tid + j * kBlock, c = (q % CH) * V;
-      *(uint4*)(sa + ((q / CH) * PITCH + c) * ESZ) =
-          pa[j] && k0 + c < g.K ? *(const uint4*)(pa[j] + (int64_t)k0 * ESZ) : zero;
+      const int r = t.r0 + tid / CH + j * (kF32Threads / CH);
+      int64_t src = -1;
+      if (r < t.r1) {
+        src = r - t.r0;
+        if (kSwiglu) {
+          src = token_of(g, g.row_pair[r]);
+          if (src < 0) set_error(g.err, LRM_DEVERR_INDEX);
+        }
+      }
+      oa[j] = src < 0 ? kOutOfRange : ((uint32_t)src * (uint32_t)g.K + kc) * 4;
     }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const int q = tid + j * kBlock, c = (q % CH) * V;
-      *(uint4*)(sb + ((q / CH) * PITCH + c) * ESZ) =
-          pb[j] && k0 + c < g.K ? *(const uint4*)(pb[j] + (int64_t)k0 * ESZ) : zero;
+      const int r = tid / CH + j * (kF32Threads / CH);   // row of the B tile
+      const int col = n0 + (kSwiglu ? r % kBNH : r);
+      const uint32_t src = (uint32_t)(col + (kSwiglu ? r / kBNH * g.N : 0));
+      ob[j] = col < g.N ? (src * (uint32_t)g.K + kc) * 4 : kOutOfRange;
     }
-    __syncthreads();
-    const int ra = wm * 32 + (lane & 31), rb = wn * 32 + (lane & 31);
-    if constexpr (kBF16) {
+    uint4 va[NA], vb[NB];
+    f32x16 acc[2], run[2];
 #pragma unroll
-      for (int ks = 0; ks < kKS; ks += 16) {
-        const int c = ks + 8 * (lane >> 5);
-        const bf16x8 a = *(const bf16x8*)(sa + (ra * PITCH + c) * 2);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bf16x8 b = *(const bf16x8*)(sb + ((rb + j * kBNH) * PITCH + c) * 2);
-          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[j], 0, 0, 0);
-        }
+      for (int i = 0; i < 16; ++i) acc[j][i] = run[j][i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NA; ++j) va[j] = load16(ra, kc < g.K ? oa[j] : kOutOfRange);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) vb[j] = load16(rb, kc < g.K ? ob[j] : kOutOfRange);
+    for (int k0 = 0; k0 < g.K; k0 += kKS) {
+      const int at = tid / CH * kPitch + kc;
+#pragma unroll
+      for (int j = 0; j < NA; ++j) *(uint4*)(sa + at + j * (kF32Threads / CH) * kPitch) = va[j];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) *(uint4*)(sb + at + j * (kF32Threads / CH) * kPitch) = vb[j];
+      __syncthreads();
+      const bool in = k0 + kKS + kc < g.K;   // past the last step every load is out of range
+#pragma unroll
+      for (int j = 0; j < NA; ++j) va[j] = load16(ra, in ? oa[j] + (k0 + kKS) * 4 : kOutOfRange);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) vb[j] = load16(rb, in ? ob[j] + (k0 + kKS) * 4 : kOutOfRange);
+      const float* fa = sa + (wm * 32 + (lane & 31)) * kPitch + 4 * (lane >> 5);
+      const float* fb = sb + (lane & 31) * kPitch + 4 * (lane >> 5);
+#pragma unroll
+      for (int ks = 0; ks < kKS; ks += 8) {
+        const float4 a = *(const float4*)(fa + ks);
+        const float4 b0 = *(const float4*)(fb + ks), b1 = *(const float4*)(fb + kBNH * kPitch + ks);
+        run[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.x, b0.x, run[0], 0, 0, 0);
+        run[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.x, b1.x, run[1], 0, 0, 0);
+        run[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.y, b0.y, run[0], 0, 0, 0);
+        run[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.y, b1.y, run[1], 0, 0, 0);
+        run[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.z, b0.z, run[0], 0, 0, 0);
+        run[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.z, b1.z, run[1], 0, 0, 0);
+        run[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.w, b0.w, run[0], 0, 0, 0);
+        run[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.w, b1.w, run[1], 0, 0, 0);
       }
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < kKS; ks += 2) {
-        const int c = ks + (lane >> 5);
-        const float a = ((const float*)sa)[ra * PITCH + c];
+      if ((k0 + kKS) % kRun == 0 || k0 + kKS >= g.K) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-              a, ((const float*)sb)[(rb + j * kBNH) * PITCH + c], acc[j], 0, 0, 0);
-      }
-    }
-    __syncthreads();
-  }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t r = t.r0 + wm * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-    if (r >= t.r1) continue;
-    const int col = n0 + wn * 32 + (lane & 31);
-    if (kSwiglu) {
-      if (col < g.N) {
-        if (g.out != nullptr) {
-          store_elem<kBF16>(g.out, r * 2 * g.N + col, acc[0][i]);
-          store_elem<kBF16>(g.out, r * 2 * g.N + g.N + col, acc[1][i]);
-        }
-        store_elem<kBF16>(g.out2, r * g.N + col, silu_mul(acc[0][i], acc[1][i]));
+          for (int i = 0; i < 16; ++i) {
+            acc[j][i] += run[j][i];
+            run[j][i] = 0.0f;
+          }
       }
-    } else {
-      if (col < g.N) store_elem<kBF16>(g.out, r * g.N + col, acc[0][i]);
-      if (col + kBNH < g.N) store_elem<kBF16>(g.out, r * g.N + col + kBNH, acc[1][i]);
+      __syncthreads();
     }
-  }
+    float* out = (float*)g.out;
+    float* phi = (float*)g.out2;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t r = t.r0 + wm * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+      const int col = n0 + (lane & 31);
+      if (r >= t.r1) continue;
+      if constexpr (kSwiglu) {
+        if (col >= g.N) continue;
+        if (out != nullptr) {
+          out[r * 2 * g.N + col] = acc[0][i];
+          out[r * 2 * g.N + g.N + col] = acc[1][i];
+        }
+        phi[r * g.N + col] = silu_mul(acc[0][i], acc[1][i]);
+      } else {
+        if (col < g.N) out[r * g.N + col] = acc[0][i];
+        if (col + kBNH < g.N) out[r * g.N + col + kBNH] = acc[1][i];
+      }
+    }
   }
 }
 
@@ -217,18 +259,8 @@ struct Shape {
   static constexpr int TABLE = 1024 + 1;                  // tiles before each expert
   static constexpr int LDS = S * STG + (TABLE + 3) / 4 * 16;
   static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(S * I < 64, "vmcnt range");
 };
-
-constexpr uint32_t kOutOfRange = 0x80000000u;
-
-// Buffer resource of 2^31 bytes from base: every offset that is used lies below what the host checked.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
-  const uint64_t v = (uint64_t)(uintptr_t)base;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), (short)0,
-                                           (int)kOutOfRange, 0x00020000);
-}
 
 // 16 bytes a lane from r + voff to LDS address lds + 16 lane.  Inline assembly, so that the compiler
 // does not wait for it before every LDS read; the pipeline orders it with vmcnt and barriers.
@@ -408,11 +440,11 @@ __device__ __forceinline__ void multiply(const Frags<C>& f, f32x16 (&acc)[C::MT]
 // Spreads the slice's LDS reads over its MFMAs.
 template <class C>
 __device__ __forceinline__ void interleave() {
-  static_assert(C::MT + C::NT <= C::MT * C::NT, "a read behind each MFMA");
+  constexpr int M = C::MT * C::NT, R = (C::MT + C::NT + M - 1) / M;   // reads behind each MFMA
 #pragma unroll
-  for (int q = 0; q < C::MT * C::NT; ++q) {
+  for (int q = 0; q < M; ++q) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
   }
 }
 
@@ -590,24 +622,21 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
 // ------------------------------------------------------------------------------------------------
 // Few rows an expert (serving steps): bound by streaming the chosen experts' weights once.
 //
-// A workgroup computes up to 16 TT tokens x 32 weight rows (for kSwiglu 16 of each half) of one expert; its four wavefronts share the contracted axis, 128 bytes of every row in turn, so that
+// A workgroup computes up to 16 TT tokens x 32 weight rows (for kSwiglu 16 of each half) of one
+// expert; its four wavefronts share the contracted axis, 128 bytes of every row in turn, so that
 // even one token's eight experts put thousands of wavefronts' loads in flight at once.  Nothing
 // goes through LDS but the four partial sums, added in a fixed order: a 16-row MFMA operand is one
 // 16-byte load a lane (16 rows x 64 bytes), which for float32 serves four MFMAs, lane group q
 // holding k = 4 q + i for the i-th (any order of k will do, as both operands have the same).
-// Rows past the segment's end read its last row again and are not stored.
+// Rows past the segment's end read its last row again and are not stored.  A tile holds the rows of
+// any batch of up to 16 TT tokens (an expert is chosen once a token), so the weights are read
+// once; the loads are temporal, as a row's 128-byte lines are read in two halves (non-temporal ones
+// fetched them twice: 18 % slower).
 // ------------------------------------------------------------------------------------------------
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kFewWaves = 4;
-#ifndef FEW_R
-#define FEW_R 5
-#endif
-#ifndef FEW_A
-#define FEW_A 2, 1
-#define FEW_B 4, 2
-#define FEW_N 2
-#endif
-constexpr int kFewAhead = FEW_N;   // 128-byte pieces of each row in flight per wavefront
+constexpr int kFewAhead = 2;   // 128-byte pieces of each row in flight per wavefront
+constexpr int WF = 2;          // 16-row weight operands
 
 template <bool kBF16>
 __device__ __forceinline__ f32x4 few_mma(uint4 a, uint4 b, f32x4 c) {
@@ -622,20 +651,15 @@ __device__ __forceinline__ f32x4 few_mma(uint4 a, uint4 b, f32x4 c) {
   }
 }
 
-// The token of pair p, or -1 for a pair id that is none.
-__device__ __forceinline__ int64_t token_of(const FcArgs& g, int p) {
-  return p >= 0 && p < g.P ? p / g.k : -1;
-}
-
 // 128 bytes of 2 x 16 weight rows and TT x 16 token rows.
-template <int WF, int TT>
+template <int TT>
 struct FewPiece {
   uint4 a[2][WF], b[2][TT];
   __device__ __forceinline__ void load(const char* const (&pw)[WF], const char* const (&pt)[TT], int64_t off) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < WF; ++i) a[h][i] = load_nt((const uint4*)(pw[i] + off + 64 * h));
+      for (int i = 0; i < WF; ++i) a[h][i] = *(const uint4*)(pw[i] + off + 64 * h);
 #pragma unroll
       for (int j = 0; j < TT; ++j) b[h][j] = *(const uint4*)(pt[j] + off + 64 * h);
     }
@@ -664,154 +688,194 @@ struct FewPiece {
   }
 };
 
-template <bool kBF16, bool kSwiglu, int WF, int TT>
-__global__ __launch_bounds__(kFewWaves * kWave) void fc_few(FcArgs g) {
+// One tile with TT token operands.
+template <bool kBF16, bool kSwiglu, int TT>
+__device__ __forceinline__ void few_tile(const FcArgs& g, const RowTile& t, int n0, int64_t u,
+                                         f32x4 (*part)[kWave]) {
   constexpr int ESZ = kBF16 ? 2 : 4, V = 16 / ESZ;
   constexpr int STEP = 128 / ESZ;              // contracted elements of a 128-byte piece
-  constexpr int BN = kSwiglu ? 8 * WF : 16 * WF;   // output columns
-  __shared__ f32x4 part[kFewWaves][WF * TT][kWave];
   const int lane = lane_id(), w = threadIdx.x / kWave;
-  const int cols = (g.N + BN - 1) / BN;
-  for (int64_t u = blockIdx.x;; u += gridDim.x) {
-    const RowTile t = find_tile<16 * TT>(g.fwd_off, g.E_loc, g.cap, (int)(u / cols));
-    if (t.e < 0) return;
-    const int n0 = (int)(u % cols) * BN;
-    const int64_t K = g.K;
-    const int k0 = (lane >> 4) * V;            // this lane's elements of a 64-byte half piece
-    const char* pw[WF];
-    const char* pt[TT];
+  const int64_t K = g.K;
+  const int k0 = (lane >> 4) * V;              // this lane's elements of a 64-byte half piece
+  const char* pt[TT];
 #pragma unroll
-    for (int i = 0; i < WF; ++i) {
-      // columns past the last one read it again
-      const int c = n0 + 16 * (kSwiglu ? i / 2 : i) + (lane & 15);
-      const int64_t row = (c < g.N ? c : g.N - 1) + (kSwiglu && i % 2 ? (int64_t)g.N : 0);
-      pw[i] = (const char*)g.B + ((int64_t)t.e * (kSwiglu ? 2 : 1) * g.N + row) * K * ESZ + k0 * ESZ;
+  for (int j = 0; j < TT; ++j) {
+    int64_t r = t.r0 + 16 * j + (lane & 15);
+    r = r < t.r1 ? r : t.r1 - 1;
+    if (kSwiglu) r = token_of(g, g.row_pair[r]);
+    pt[j] = (const char*)g.A + ((r < 0 ? 0 : r) * K + k0) * ESZ;   // a bad pair's outputs: below
+  }
+  const char* pw[WF];
+#pragma unroll
+  for (int i = 0; i < WF; ++i) {
+    // columns past the last one read it again
+    const int c = n0 + (kSwiglu ? 0 : 16 * i) + (lane & 15);
+    const int64_t row = (c < g.N ? c : g.N - 1) + (kSwiglu && i ? (int64_t)g.N : 0);
+    pw[i] = (const char*)g.B + ((int64_t)t.e * (kSwiglu ? 2 : 1) * g.N + row) * K * ESZ + k0 * ESZ;
+  }
+  f32x4 acc[WF][TT];
+#pragma unroll
+  for (int i = 0; i < WF; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  // whole 128-byte pieces of the rows, this wavefront's w, w + 4, ..; then the row's rest
+  const int whole = g.K / STEP;
+  FewPiece<TT> f[kFewAhead];
+  if (whole > 0) {
+    // the loads run ahead without a condition, so that each wait is for one piece's loads alone;
+    // past the end they fetch the last piece again
+    const int last = whole - 1;
+#pragma unroll
+    for (int q = 0; q < kFewAhead; ++q) {
+      const int c = w + q * kFewWaves;
+      f[q].load(pw, pt, (int64_t)(c < last ? c : last) * 128);
     }
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      int64_t r = t.r0 + 16 * j + (lane & 15);
-      r = r < t.r1 ? r : t.r1 - 1;
-      if (kSwiglu) r = token_of(g, g.row_pair[r]);
-      pt[j] = (const char*)g.A + ((r < 0 ? 0 : r) * K + k0) * ESZ;   // a bad pair's outputs: below
-    }
-    f32x4 acc[WF][TT];
-#pragma unroll
-    for (int i = 0; i < WF; ++i)
-#pragma unroll
-      for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    // whole 128-byte pieces of the rows, this wavefront's w, w + 4, ..; then the row's rest
-    const int whole = g.K / STEP;
-    FewPiece<WF, TT> f[kFewAhead];
-    if (whole > 0) {
-      // the loads run ahead without a condition, so that each wait is for one piece's loads alone;
-      // past the end they fetch the last piece again
-      const int last = whole - 1, turn = (int)(u * FEW_R % whole);
-      auto at = [&](int c) {
-        c = (c < last ? c : last) + turn;
-        return (int64_t)(c < whole ? c : c - whole) * 128;
-      };
+    for (int c = w; c < whole; c += kFewAhead * kFewWaves) {
 #pragma unroll
       for (int q = 0; q < kFewAhead; ++q) {
-        const int c = w + q * kFewWaves;
-        f[q].load(pw, pt, at(c));
-      }
-      for (int c = w; c < whole; c += kFewAhead * kFewWaves) {
-#pragma unroll
-        for (int q = 0; q < kFewAhead; ++q) {
-          if (c + q * kFewWaves < whole) f[q].template multiply<kBF16>(acc);
-          const int next = c + (kFewAhead + q) * kFewWaves;
-          f[q].load(pw, pt, at(next));
-        }
+        if (c + q * kFewWaves < whole) f[q].template multiply<kBF16>(acc);
+        const int next = c + (kFewAhead + q) * kFewWaves;
+        f[q].load(pw, pt, (int64_t)(next < last ? next : last) * 128);
       }
     }
-    if (g.K % STEP && whole % kFewWaves == w) {
-      f[0].load_rest(pw, pt, (int64_t)whole * 128, g.K - whole * STEP - k0, STEP / 2);
-      f[0].template multiply<kBF16>(acc);
+  }
+  if (g.K % STEP && whole % kFewWaves == w) {
+    f[0].load_rest(pw, pt, (int64_t)whole * 128, g.K - whole * STEP - k0, STEP / 2);
+    f[0].template multiply<kBF16>(acc);
+  }
+  // part[(wavefront, weight operand, token operand)]
+#pragma unroll
+  for (int i = 0; i < WF; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) part[(w * WF + i) * TT + j][lane] = acc[i][j];
+  __syncthreads();
+  // the wavefronts end the output operands in turn: lane l holds columns 4 (l / 16) + 0..3 of token
+  // l % 16
+  constexpr int OF = kSwiglu ? 1 : WF;
+  for (int o = w; o < OF * TT; o += kFewWaves) {
+    const int ci = o / TT, ti = o % TT;
+    const int64_t r = t.r0 + 16 * ti + (lane & 15);
+    f32x4 v = part[ci * TT + ti][lane], x = v;
+#pragma unroll
+    for (int q = 1; q < kFewWaves; ++q) v += part[(q * WF + ci) * TT + ti][lane];
+    if constexpr (kSwiglu) {
+      x = part[TT + ti][lane];
+#pragma unroll
+      for (int q = 1; q < kFewWaves; ++q) x += part[(q * WF + 1) * TT + ti][lane];
     }
-#pragma unroll
-    for (int i = 0; i < WF; ++i)
-#pragma unroll
-      for (int j = 0; j < TT; ++j) part[w][i * TT + j][lane] = acc[i][j];
-    __syncthreads();
-    // the (column, token) fragments are ended by the wavefronts in turn: lane l holds columns
-    // 4 (l / 16) + 0..3 of token l % 16
-    constexpr int OF = kSwiglu ? WF / 2 : WF;   // output fragments along the columns
-    for (int o = w; o < OF * TT; o += kFewWaves) {
-      const int ci = o / TT, ti = o % TT;
-      const int64_t r = t.r0 + 16 * ti + (lane & 15);
-      f32x4 v = part[0][(kSwiglu ? 2 * ci : ci) * TT + ti][lane], x = v;
-#pragma unroll
-      for (int q = 1; q < kFewWaves; ++q) v += part[q][(kSwiglu ? 2 * ci : ci) * TT + ti][lane];
-      if constexpr (kSwiglu) {
-        x = part[0][(2 * ci + 1) * TT + ti][lane];
-#pragma unroll
-        for (int q = 1; q < kFewWaves; ++q) x += part[q][(2 * ci + 1) * TT + ti][lane];
+    if (r < t.r1) {
+      if (kSwiglu && token_of(g, g.row_pair[r]) < 0) {   // reads x as zeros
+        v = x = (f32x4){0.f, 0.f, 0.f, 0.f};
+        set_error(g.err, LRM_DEVERR_INDEX);
       }
-      if (r < t.r1) {
-        if (kSwiglu && token_of(g, g.row_pair[r]) < 0) {   // reads x as zeros
-          v = x = (f32x4){0.f, 0.f, 0.f, 0.f};
-          set_error(g.err, LRM_DEVERR_INDEX);
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = n0 + 16 * ci + 4 * (lane >> 4) + i;
-          if (c >= g.N) continue;
-          if constexpr (kSwiglu) {
-            if (g.out != nullptr) {
-              store_elem<kBF16>(g.out, r * 2 * g.N + c, v[i]);
-              store_elem<kBF16>(g.out, r * 2 * g.N + g.N + c, x[i]);
-            }
-            store_elem<kBF16>(g.out2, r * g.N + c, silu_mul(v[i], x[i]));
-          } else {
-            store_elem<kBF16>(g.out, r * g.N + c, v[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int c = n0 + 16 * ci + 4 * (lane >> 4) + i;
+        if (c >= g.N) continue;
+        if constexpr (kSwiglu) {
+          if (g.out != nullptr) {
+            store_elem<kBF16>(g.out, r * 2 * g.N + c, v[i]);
+            store_elem<kBF16>(g.out, r * 2 * g.N + g.N + c, x[i]);
           }
+          store_elem<kBF16>(g.out2, r * g.N + c, silu_mul(v[i], x[i]));
+        } else {
+          store_elem<kBF16>(g.out, r * g.N + c, v[i]);
         }
       }
     }
-    __syncthreads();
+  }
+  __syncthreads();
+}
+
+template <bool kBF16, bool kSwiglu, int TT>
+__global__ __launch_bounds__(kFewWaves * kWave) void fc_few(FcArgs g) {
+  constexpr int BN = kSwiglu ? 16 : 32;        // output columns
+  __shared__ f32x4 part[kFewWaves * WF * TT][kWave];
+  const int cols = (g.N + BN - 1) / BN;
+  for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {
+    const RowTile t = find_tile<16 * TT>(g.fwd_off, g.E_loc, g.cap, u / cols);
+    if (t.e < 0) return;
+    const int n0 = (int)(u % cols) * BN, rows = t.r1 - t.r0;
+    // as many token operands as the tile's rows need
+    if (TT > 2 && rows > 32)
+      few_tile<kBF16, kSwiglu, TT>(g, t, n0, u, part);
+    else if (TT > 1 && rows > 16)
+      few_tile<kBF16, kSwiglu, 2>(g, t, n0, u, part);
+    else
+      few_tile<kBF16, kSwiglu, 1>(g, t, n0, u, part);
   }
 }
 
-template <bool kBF16, bool kSwiglu, int WF, int TT>
-void launch_few(const lrm_problem& p, const FcArgs& g, hipStream_t s) {
-  const int bn = kSwiglu ? 8 * WF : 16 * WF, rows = 16 * TT;
-  const int64_t most = (int64_t)p.L_cap / rows + p.E_loc;   // tiles, if every expert's last is partial
-  const int64_t units = (most < p.L_cap ? most : p.L_cap) * ((g.N + bn - 1) / bn);
-  hipLaunchKernelGGL((fc_few<kBF16, kSwiglu, WF, TT>), dim3((unsigned)(units < (1 << 20) ? units : 1 << 20)),
-                     dim3(kFewWaves * kWave), 0, s, g);
+// Upper bound of the row tiles of bm rows: every expert's last may be partial, and none is empty.
+inline int64_t most_tiles(const lrm_problem& p, int bm) {
+  const int64_t most = (int64_t)p.L_cap / bm + p.E_loc;
+  return most < p.L_cap ? most : p.L_cap;
+}
+
+inline unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 20) ? units : 1 << 20); }
+
+template <bool kBF16, bool kSwiglu, int TT>
+void launch_few(const lrm_problem& p, FcArgs g, hipStream_t s) {
+  const int bn = kSwiglu ? 16 : 32;
+  g.units = most_tiles(p, 16 * TT) * ((g.N + bn - 1) / bn);
+  hipLaunchKernelGGL((fc_few<kBF16, kSwiglu, TT>), dim3(grid_of(g.units)), dim3(kFewWaves * kWave), 0, s, g);
 }
 
 // Workgroups of the persistent products: one a CU, a multiple of the dies.
 constexpr int kDies = 8, kCUs = 256;
 
-#ifndef LRM_FC_SHAPE
-#define LRM_FC_SHAPE 4, 2, 2, 4, 2
-#endif
+// The bf16 tiles, by tokens x weight rows.  Measured over a whole layer of 128 experts (h 2048, d 768,
+// Zipf-skewed top-8 routing), us of FC1 / FC2 with Low, Mid, Big:
+//   256 tokens   67 / 35   85 / 41   80 / 57      (16 rows an expert on average)
+//   512          91 / 47   93 / 43  130 / 57      (32)
+//  2048         214 / 117 165 / 101 189 / 103     (128)
+//  4096         387 / 213 292 / 162 301 / 162     (256)
+// and over a 16-expert share (h 4096, d 1408) at 2048 tokens 598 / 310, 427 / 234, 361 / 218.
+using Low = Shape<2, 2, 2, 1, 3>;   // 64 x 128
+using Mid = Shape<4, 2, 2, 2, 3>;   // 128 x 256
+using Big = Shape<4, 2, 2, 4, 2>;   // 256 x 256
+constexpr int kMidRows = 24, kBigRows = 256;
+// Tokens up to which fc_few is the faster one: bf16 FC1 / FC2 of one token 16.7 / 9.0 against Low's
+// 18.1 / 10.5, of four 22.3 / 12.9 against 22.5 / 12.1; float32 (h = d = 512, 32 experts) 27 / 19 against
+// fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at 256.
+constexpr int kFewBF16 = 2, kFewF32 = 128;
 
-template <bool kSwiglu>
-hipError_t launch_fc(const lrm_problem& p, const FcArgs& g, hipStream_t s) {
-  const int bn = kSwiglu ? kBNH : 2 * kBNH;
-  // every expert's last tile may be partial
-  const int64_t units = (((int64_t)p.L_cap + kBM - 1) / kBM + p.E_loc) * ((g.N + bn - 1) / bn);
-  const dim3 grid((unsigned)(units < (1 << 20) ? units : 1 << 20));
-  using Big = Shape<LRM_FC_SHAPE>;
-  const int few = getenv("LRM_FEW") ? atoi(getenv("LRM_FEW")) : 16;
-  if (p.L_cap <= (int64_t)few * p.E_loc) {
-    const bool one = p.L_cap <= 4 * (int64_t)p.E_loc;
-    if (p.dtype == LRM_BF16) {
-      if (one) launch_few<true, kSwiglu, FEW_A>(p, g, s);
-      else launch_few<true, kSwiglu, FEW_B>(p, g, s);
-    } else {
-      if (one) launch_few<false, kSwiglu, FEW_A>(p, g, s);
-      else launch_few<false, kSwiglu, FEW_B>(p, g, s);
-    }
-  } else if (p.dtype == LRM_BF16 && p.L_cap >= (getenv("LRM_BIG") ? atoi(getenv("LRM_BIG")) : 128) * (int64_t)p.E_loc)
-    hipLaunchKernelGGL((fc_bf16<Big, kSwiglu>), dim3(kCUs), dim3(Big::THREADS), 0, s, g, kDies);
-  else if (p.dtype == LRM_BF16)
-    hipLaunchKernelGGL((fc_tile<true, kSwiglu>), grid, dim3(kBlock), 0, s, g);
-  else
-    hipLaunchKernelGGL((fc_tile<false, kSwiglu>), grid, dim3(kBlock), 0, s, g);
+template <class C, bool kSwiglu>
+hipError_t launch_shape(const FcArgs& g, hipStream_t s) {
+  constexpr int per_cu = 160 * 1024 / C::LDS;
+  hipLaunchKernelGGL((fc_bf16<C, kSwiglu>), dim3(kCUs * per_cu), dim3(C::THREADS), 0, s, g, kDies);
   return hipGetLastError();
+}
+
+template <bool kBF16, bool kSwiglu>
+hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
+  if (p.T <= (kBF16 ? kFewBF16 : kFewF32)) {   // an expert is chosen once a token: T rows at most
+    if constexpr (kBF16) {
+      launch_few<kBF16, kSwiglu, 1>(p, g, s);
+    } else {
+      if (p.T <= 16)
+        launch_few<kBF16, kSwiglu, 1>(p, g, s);
+      else if (p.T <= 32)
+        launch_few<kBF16, kSwiglu, 2>(p, g, s);
+      else
+        launch_few<kBF16, kSwiglu, 4>(p, g, s);
+    }
+    return hipGetLastError();
+  }
+  if constexpr (kBF16) {
+    // rows of an expert: the capacity's share, unless that is far above the balanced load T k / E (a
+    // share of a layer has capacity for every pair)
+    const int64_t cap = (int64_t)p.L_cap / p.E_loc, most = 4 * ((int64_t)p.T * p.k / p.E);
+    const int64_t rows = cap < most ? cap : most;
+    if (rows >= kBigRows) return launch_shape<Big, kSwiglu>(g, s);
+    if (rows >= kMidRows) return launch_shape<Mid, kSwiglu>(g, s);
+    return launch_shape<Low, kSwiglu>(g, s);
+  } else {
+    const int bn = kSwiglu ? kBNH : 2 * kBNH;
+    g.units = most_tiles(p, kBM) * ((g.N + bn - 1) / bn);
+    hipLaunchKernelGGL((fc_f32<kSwiglu>), dim3(grid_of(g.units)), dim3(kF32Threads), 0, s, g);
+    return hipGetLastError();
+  }
 }
 
 // map[row_pair[r]] = r for every forward row; a pair id outside [0, P) sets LRM_DEVERR_INDEX.
@@ -998,15 +1062,15 @@ hipError_t launch_fc1_swiglu(const lrm_problem& p, const int32_t* row_pair, cons
                              const void* x, const void* W1, void* ac, void* phi, char* ws,
                              hipStream_t s) {
   const FcArgs g{x, W1, row_pair, fwd_off, (int64_t)p.T * p.k, p.E_loc, p.L_cap, p.k, p.h, p.d,
-                 ac, phi, (int32_t*)ws};
-  return launch_fc<true>(p, g, s);
+                 ac, phi, (int32_t*)ws, 0};
+  return p.dtype == LRM_BF16 ? launch_fc<true, true>(p, g, s) : launch_fc<false, true>(p, g, s);
 }
 
 hipError_t launch_fc2(const lrm_problem& p, const int32_t* fwd_off, const void* phi, const void* W,
                       void* y, hipStream_t s) {
   const FcArgs g{phi, W, nullptr, fwd_off, (int64_t)p.T * p.k, p.E_loc, p.L_cap, p.k, p.d, p.h,
-                 y, nullptr, nullptr};
-  return launch_fc<false>(p, g, s);
+                 y, nullptr, nullptr, 0};
+  return p.dtype == LRM_BF16 ? launch_fc<true, false>(p, g, s) : launch_fc<false, false>(p, g, s);
 }
 
 hipError_t launch_combine(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,

@@ -583,8 +583,8 @@ lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row
  * expert i (float32 accumulation).
  *  in : fwd_off int32 [E_loc+1]; phi [L_cap][d]; W [E_loc][h][d]
  *  out: y [L_cap][h] (first L rows written)
- * One expert's weights must not exceed 2^31 bytes (LRM_ERR_UNSUPPORTED).  phi, W and y 16-byte
- * aligned.
+ * One expert's weights must not exceed 2^31 bytes, nor a row of phi 2^23 (LRM_ERR_UNSUPPORTED).
+ * phi, W and y 16-byte aligned.
  */
 lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
                            const void* W, void* y, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -77,6 +77,8 @@ def test_forward_refusals():
     wide = _problem(T=16, h=2 ** 15, d=2 ** 15 + 8)
     assert lib.lrm_grouped_fc1_swiglu(ctypes.byref(wide), *[FAKE] * 7, 1 << 40, None) == 2
     assert lib.lrm_grouped_fc2(ctypes.byref(wide), *[FAKE] * 5, 1 << 40, None) == 2
+    long_rows = _problem(T=16, h=8, d=2 ** 22 + 8)
+    assert lib.lrm_grouped_fc2(ctypes.byref(long_rows), *[FAKE] * 5, 1 << 40, None) == 2
     for i in range(4):
         a = [FAKE] * 5
         a[i] = None
