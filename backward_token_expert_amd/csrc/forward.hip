@@ -110,27 +110,26 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
 // float32 products: 64 rows x 64 columns (for kSwiglu 32 of each half) by 2 wavefronts, each one 32
 // rows x two 32-wide column tiles, which for kSwiglu are the same columns of the gate and the up
 // half.  Bound by the float32 matrix rate (64 cycles an MFMA, against one 16-byte LDS read a lane
-// for four of them): the next K step's loads are in registers while one is multiplied, and the
-// workgroups of a CU (eight, small ones, so that the last round of a small layer is short) cover
-// each other's barriers.  A lane's 16 bytes hold four k of one row; the i-th
+// for four of them): the next K step's loads are in registers while one is multiplied, and a CU's
+// many small workgroups cover each other's barriers.  A lane's 16 bytes hold four k of one row; the i-th
 // MFMA takes the i-th of both operands, so k = 8 s + i and 8 s + 4 + i meet, in any order.
-// Rows of 128 k are summed apart and then added, which keeps the error of a long row's sum near
-// that of a short one's.
+// kLong: runs of 128 k are summed apart and then added, so that a long row's sum is no less exact
+// than a short one's; without the second set of accumulators 12 workgroups fit a CU, not 8.
 // ------------------------------------------------------------------------------------------------
-constexpr int kBM = 64, kBNH = 32, kKS = 16, kPitch = kKS + 4, kRun = 128, kF32Threads = 128;
+constexpr int kBM = 64, kBNH = 64, kKS = 16, kPitch = kKS + 4, kRun = 128, kLongK = 512, kF32Threads = 256;
 
 __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-template <bool kSwiglu>
-__global__ __launch_bounds__(kF32Threads, 4) void fc_f32(FcArgs g) {
+template <bool kSwiglu, bool kLong>
+__global__ __launch_bounds__(kF32Threads, kLong ? 4 : 6) void fc_f32(FcArgs g) {
   constexpr int CH = kKS / 4;
   constexpr int NA = kBM * CH / kF32Threads, NB = 2 * kBNH * CH / kF32Threads;   // chunks a thread moves
   __shared__ __attribute__((aligned(16))) float sa[kBM * kPitch];
   __shared__ __attribute__((aligned(16))) float sb[2 * kBNH * kPitch];
   const int cols = (g.N + (kSwiglu ? kBNH : 2 * kBNH) - 1) / (kSwiglu ? kBNH : 2 * kBNH);
-  const int tid = threadIdx.x, lane = lane_id(), wm = tid / kWave;
+  const int tid = threadIdx.x, lane = lane_id(), wm = tid / kWave / 2, wn = tid / kWave % 2;
   const int kc = (tid % CH) * 4;   // this thread's k of a step
   for (int64_t u = blockIdx.x; u < g.units; u += gridDim.x) {   // unit = (row tile, column tile)
     const RowTile t = find_tile<kBM>(g.fwd_off, g.E_loc, g.cap, u / cols);
@@ -165,7 +164,7 @@ __global__ __launch_bounds__(kF32Threads, 4) void fc_f32(FcArgs g) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[j][i] = run[j][i] = 0.0f;
+      for (int i = 0; i < 16; ++i) acc[j][i] = run[j][i] = 0.0f;   // acc: only for kLong
 #pragma unroll
     for (int j = 0; j < NA; ++j) va[j] = load16(ra, kc < g.K ? oa[j] : kOutOfRange);
 #pragma unroll
@@ -182,8 +181,9 @@ __global__ __launch_bounds__(kF32Threads, 4) void fc_f32(FcArgs g) {
       for (int j = 0; j < NA; ++j) va[j] = load16(ra, in ? oa[j] + (k0 + kKS) * 4 : kOutOfRange);
 #pragma unroll
       for (int j = 0; j < NB; ++j) vb[j] = load16(rb, in ? ob[j] + (k0 + kKS) * 4 : kOutOfRange);
+      __builtin_amdgcn_sched_barrier(0);   // a whole step ahead of their use
       const float* fa = sa + (wm * 32 + (lane & 31)) * kPitch + 4 * (lane >> 5);
-      const float* fb = sb + (lane & 31) * kPitch + 4 * (lane >> 5);
+      const float* fb = sb + (wn * 32 + (lane & 31)) * kPitch + 4 * (lane >> 5);
 #pragma unroll
       for (int ks = 0; ks < kKS; ks += 8) {
         const float4 a = *(const float4*)(fa + ks);
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kF32Threads, 4) void fc_f32(FcArgs g) {
         run[0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.w, b0.w, run[0], 0, 0, 0);
         run[1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a.w, b1.w, run[1], 0, 0, 0);
       }
-      if ((k0 + kKS) % kRun == 0 || k0 + kKS >= g.K) {
+      if (kLong && ((k0 + kKS) % kRun == 0 || k0 + kKS >= g.K)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -208,23 +208,24 @@ __global__ __launch_bounds__(kF32Threads, 4) void fc_f32(FcArgs g) {
       }
       __syncthreads();
     }
+    const f32x16(&sum)[2] = kLong ? acc : run;
     float* out = (float*)g.out;
     float* phi = (float*)g.out2;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int64_t r = t.r0 + wm * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-      const int col = n0 + (lane & 31);
+      const int col = n0 + wn * 32 + (lane & 31);
       if (r >= t.r1) continue;
       if constexpr (kSwiglu) {
         if (col >= g.N) continue;
         if (out != nullptr) {
-          out[r * 2 * g.N + col] = acc[0][i];
-          out[r * 2 * g.N + g.N + col] = acc[1][i];
+          out[r * 2 * g.N + col] = sum[0][i];
+          out[r * 2 * g.N + g.N + col] = sum[1][i];
         }
-        phi[r * g.N + col] = silu_mul(acc[0][i], acc[1][i]);
+        phi[r * g.N + col] = silu_mul(sum[0][i], sum[1][i]);
       } else {
-        if (col < g.N) out[r * g.N + col] = acc[0][i];
-        if (col + kBNH < g.N) out[r * g.N + col + kBNH] = acc[1][i];
+        if (col < g.N) out[r * g.N + col] = sum[0][i];
+        if (col + kBNH < g.N) out[r * g.N + col + kBNH] = sum[1][i];
       }
     }
   }
@@ -873,7 +874,10 @@ hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
   } else {
     const int bn = kSwiglu ? kBNH : 2 * kBNH;
     g.units = most_tiles(p, kBM) * ((g.N + bn - 1) / bn);
-    hipLaunchKernelGGL((fc_f32<kSwiglu>), dim3(grid_of(g.units)), dim3(kF32Threads), 0, s, g);
+    if (g.K > kLongK)
+      hipLaunchKernelGGL((fc_f32<kSwiglu, true>), dim3(grid_of(g.units)), dim3(kF32Threads), 0, s, g);
+    else
+      hipLaunchKernelGGL((fc_f32<kSwiglu, false>), dim3(grid_of(g.units)), dim3(kF32Threads), 0, s, g);
     return hipGetLastError();
   }
 }

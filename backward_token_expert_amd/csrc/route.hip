@@ -790,7 +790,7 @@ unsigned launch_rows_e(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
   // few tokens: more lanes each, for the latency of one token's chain (one token 10.4 us with 4
   // lanes, 7.3 with 8, 5.8 with 16); 32768 tokens take 21.8, 21.7 and 23.9 us
   if (a.E <= 128 && a.T <= kShortBatch) return launch_rows<kBF16, 16, 8, KT, 8>(a, o, s);
-  if (a.E <= 128) return launch_rows<kBF16, 8, 16, KT, 8>(a, o, s);
+  if (a.E <= 128) return launch_rows<kBF16, 8, 16, KT, 16>(a, o, s);
   if (a.E <= 256) return launch_rows<kBF16, 8, 32, KT, 8>(a, o, s);
   if (a.E <= 512) return launch_rows<kBF16, 16, 32, KT, 4>(a, o, s);
   return launch_rows<kBF16, 64, 64, KT, 2>(a, o, s);
