@@ -64,6 +64,12 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ fwd_off
 
 __device__ __forceinline__ float silu_mul(float a, float c) { return a / (1.0f + expf(-a)) * c; }
 
+// The same with the hardware's power of two and reciprocal (each off by about 2^-23), for outputs that
+// are rounded to bf16: the exact forms took 7 % of FC1's time.  exp(-a) = infinity gives 0, as it should.
+__device__ __forceinline__ float silu_mul_fast(float a, float c) {
+  return a * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.44269504f)) * c;
+}
+
 template <bool kBF16>
 __device__ __forceinline__ void store_elem(void* base, int64_t i, float v) {
   if (kBF16)
@@ -238,11 +244,18 @@ __global__ __launch_bounds__(kF32Threads, kLong ? 4 : 6) void fc_f32(FcArgs g) {
 // tiles of 32 x 32, the weights as the MFMA's row operand and the tokens as its columns, so a
 // lane's accumulators hold consecutive outputs of one token.  For kSwiglu the weight rows of the
 // tile are dealt in 32-row groups, gate, up, gate, up, .., so that both halves of an output column
-// meet in one lane.  Both operands contract over their contiguous axis: K steps of BK elements go
-// from global memory straight to an LDS ring of S stages (rows of BK elements, 16-byte chunks
-// XOR-swizzled so that 32 rows read at one k land on different banks), the rows of x gathered by the
-// load's per-lane offset.  A row or chunk that is not there (past the segment, past K, no valid
-// token) gets an offset beyond the buffer's range and reads as zero.
+// meet in one lane.  Both operands contract over their contiguous axis: K steps of 64 elements go
+// from global memory straight to an LDS ring of S stages, the rows of x gathered by the load's
+// per-lane offset.  One barrier a step, before its last slice: by then every wavefront holds that
+// slice in registers, so the stage is free for the step S on, whose loads go out behind it.
+// Workgroups are persistent; each die has a range of units of its own, whose panels share its L2.
+//
+// Bound by the matrix units at the clock that power leaves (1.6 GHz, 61 % busy), then by the loads:
+// with every panel in L2 the GLM4.5 share's FC1 would be 8 % faster.  Measured: that FC1 (250k rows,
+// h 4096, d 1408) 5.13-5.17 ms, 1120 TFLOP/s (a library product of 8192^3: 1314); FC2 of the Qwen3 share
+// (250k rows, h 2048, d 768) 832 us, 945 TFLOP/s, a fifth of it outputs.  Tried and slower: four
+// wavefronts of 128 x 128 (953), K steps of 32 in four stages (1054), waiting for the last unit's
+// stores a step later (1091), staggered workgroups, blocks of 4 or 16 row tiles.
 // ------------------------------------------------------------------------------------------------
 constexpr int BK = 64;                                    // K step: rows of 128 bytes in LDS
 constexpr int CH = 8;                                     // their 16-byte chunks
@@ -258,7 +271,11 @@ struct Shape {
   static constexpr int IT = T_BYTES / 1024 / NW, IW = W_BYTES / 1024 / NW, I = IT + IW;
   static_assert(IT * 1024 * NW == T_BYTES && IW * 1024 * NW == W_BYTES, "whole 1 KiB blocks a wave");
   static constexpr int TABLE = 1024 + 1;                  // tiles before each expert
-  static constexpr int LDS = S * STG + (TABLE + 3) / 4 * 16;
+  // FC2's outputs go through 2 KiB of LDS a wavefront where as many workgroups still fit a CU.
+  static constexpr int TABLE_BYTES = (TABLE + 3) / 4 * 16, OUT_BYTES = NW * 2048;
+  static constexpr bool STAGED =
+      160 * 1024 / (S * STG + TABLE_BYTES + OUT_BYTES) == 160 * 1024 / (S * STG + TABLE_BYTES);
+  static constexpr int LDS = S * STG + TABLE_BYTES + (STAGED ? OUT_BYTES : 0);
   static_assert(LDS <= 160 * 1024, "LDS");
   static_assert(S * I < 64, "vmcnt range");
 };
@@ -449,24 +466,68 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-// 8 outputs of one token per lane and 16-column group: accumulators hold columns 8 g + 4 (l / 32)
-// + 0..3 of token l % 32 for g = 0..3; the halves of two groups change places between lanes l and
-// l + 32, so that each lane has 8 consecutive columns to store in one 16-byte access.
-__device__ __forceinline__ void store_tile(uint16_t* row, int col, int N, int lane, const float (&v)[16]) {
+// 32 outputs of each of 32 tokens as bf16.  Accumulators hold columns 8 g + 4 (l / 32) + 0..3 of token
+// l % 32 for g = 0..3; the halves of two groups change places between lanes l and l + 32, so that
+// each lane has 8 consecutive columns: q[h] those from column 16 h + 8 (l / 32).
+__device__ __forceinline__ void pack_tile(const float (&v)[16], uint4 (&q)[2]) {
   uint32_t p[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) p[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t q[4];
+    const auto x = __builtin_amdgcn_permlane32_swap(p[4 * h], p[4 * h + 2], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(p[4 * h + 1], p[4 * h + 3], false, false);
+    q[h] = make_uint4(x[0], y[0], x[1], y[1]);
+  }
+}
+
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// n packed 32-column tiles of 32 tokens from row r0 to out (rows of `pitch` elements, columns from
+// `col`, those below `end` only, rows below r1 only), from where the lanes hold them: an instruction
+// writes 32 rows by 32 bytes.
+template <int n>
+__device__ __forceinline__ void store_direct(const uint4 (&q)[n][2], uint16_t* out, int64_t pitch,
+                                             int64_t r0, int64_t r1, int col, int end, int lane) {
+  const int64_t r = r0 + (lane & 31);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const auto x = __builtin_amdgcn_permlane32_swap(p[4 * h + i], p[4 * h + 2 + i], false, false);
-      q[i] = x[0];
-      q[2 + i] = x[1];
+  for (int i = 0; i < n; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = col + 32 * i + 16 * h + 8 * (lane >> 5);
+      if (r < r1 && c < end) *(uint4*)(out + r * pitch + c) = q[i][h];
     }
-    const int c = col + 16 * h + 8 * (lane >> 5);
-    if (row != nullptr && c < N) *(uint4*)(row + c) = make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// The same two tiles through `stage` (2 KiB of LDS, this wavefront's), 16 tokens at a time: an
+// instruction writes 8 rows by 128 bytes.  FC2's outputs are 20 % of its time (a copy that stores
+// nothing takes 673 us where the Qwen3 share takes 840 to 868); this saves 3 % of it.  FC1's, whose two
+// halves and phi come in runs of 64 bytes a wavefront, were no faster this way.
+__device__ __forceinline__ void store_staged(const uint4 (&q)[2][2], uint16_t* out, int64_t pitch,
+                                             int64_t r0, int64_t r1, int col, int end, int lane,
+                                             char* stage) {
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int tok = (lane & 31) - 16 * pass;
+    if (tok >= 0 && tok < 16) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *(uint4*)(stage + tok * 128 + (((4 * i + 2 * h + (lane >> 5)) ^ tok) & 7) * 16) = q[i][h];
+    }
+    wave_fence();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = 8 * k + lane / 8, c = lane % 8;
+      const uint4 v = *(const uint4*)(stage + t * 128 + ((c ^ t) & 7) * 16);
+      const int64_t r = r0 + 16 * pass + t;
+      if (r < r1 && col + 8 * c < end) *(uint4*)(out + r * pitch + col + 8 * c) = v;
+    }
+    wave_fence();
   }
 }
 
@@ -587,32 +648,40 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
       __builtin_amdgcn_sched_barrier(0);
       cur = next;
     }
+    static_assert(C::MT == 2, "a wavefront's columns: one gate and up pair, or two tiles");
 #pragma unroll
     for (int j = 0; j < C::NT; ++j) {
-      const int64_t r = t.r0 + (wt * C::NT + j) * 32 + (lane & 31);
-      const bool in = r < t.r1;
+      const int64_t r0 = t.r0 + (wt * C::NT + j) * 32;
+      float v[16];
+      if constexpr (kSwiglu) {
+        const int col = t.n0 + ww * 32;
+        uint4 q[1][2];
+        if (g.out != nullptr) {
 #pragma unroll
-      for (int i = 0; i < C::MT; i += kSwiglu ? 2 : 1) {
-        float v[16];
-        if constexpr (kSwiglu) {
-          const int col = t.n0 + (ww * C::MT + i) * 16;
-          uint16_t* ac = in && g.out != nullptr ? (uint16_t*)g.out + r * 2 * g.N : nullptr;
-          if (g.out != nullptr) {
+          for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
-            store_tile(ac, col, g.N, lane, v);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = acc[i + 1][j][q];
-            store_tile(ac != nullptr ? ac + g.N : nullptr, col, g.N, lane, v);
+            for (int k = 0; k < 16; ++k) v[k] = acc[i][j][k];
+            pack_tile(v, q[0]);
+            store_direct<1>(q, (uint16_t*)g.out + i * g.N, 2 * g.N, r0, t.r1, col, g.N, lane);
           }
-#pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = silu_mul(acc[i][j][q], acc[i + 1][j][q]);
-          store_tile(in ? (uint16_t*)g.out2 + r * g.N : nullptr, col, g.N, lane, v);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
-          store_tile(in ? (uint16_t*)g.out + r * g.N : nullptr, t.n0 + (ww * C::MT + i) * 32, g.N, lane, v);
         }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = silu_mul_fast(acc[0][j][k], acc[1][j][k]);
+        pack_tile(v, q[0]);
+        store_direct<1>(q, (uint16_t*)g.out2, g.N, r0, t.r1, col, g.N, lane);
+      } else {
+        uint4 q[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = acc[i][j][k];
+          pack_tile(v, q[i]);
+        }
+        if constexpr (C::STAGED)
+          store_staged(q, (uint16_t*)g.out, g.N, r0, t.r1, t.n0 + ww * 64, g.N, lane,
+                       lds + C::S * C::STG + C::TABLE_BYTES + wave * 2048);
+        else
+          store_direct<2>(q, (uint16_t*)g.out, g.N, r0, t.r1, t.n0 + ww * 64, g.N, lane);
       }
     }
     // the loader is in the next unit, unless units are so short that it is past it already
