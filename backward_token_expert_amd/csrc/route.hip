@@ -92,20 +92,19 @@ struct RouteArgs {
 };
 
 // One wavefront per token, any E and k: k rounds, each taking the largest key below the last one
-// over the row (which stays in the caches).  The workgroup's waves keep sums of probabilities and
-// counts of their own in LDS.
+// over the row (which stays in the caches).  The workgroup's waves keep sums of probabilities of
+// their own, and counts together, in LDS.
 constexpr int kAnyWaves = 2;
 
 template <bool kBF16>
 __global__ __launch_bounds__(kAnyWaves * kWave) void route_any(RouteArgs a) {
   extern __shared__ float shared[];
   const int E = a.E, lane = lane_id(), w = threadIdx.x / kWave;
-  float* prob = shared + w * E;                             // [waves][E]
-  int* counts = (int*)(shared + kAnyWaves * E) + w * E;     // [waves][E]
-  for (int e = lane; e < E; e += kWave) {
-    prob[e] = 0.0f;
-    counts[e] = 0;
-  }
+  float* prob = shared + w * E;                     // [waves][E]
+  int* counts = (int*)(shared + kAnyWaves * E);     // [E]
+  for (int e = lane; e < E; e += kWave) prob[e] = 0.0f;
+  for (int e = threadIdx.x; e < E; e += kAnyWaves * kWave) counts[e] = 0;
+  __syncthreads();
   int live = 0, bad = 0;
   const int nw = gridDim.x * kAnyWaves;
   for (int64_t t = (int64_t)blockIdx.x * kAnyWaves + w; t < a.T; t += nw) {
@@ -153,7 +152,7 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void route_any(RouteArgs a) {
         const int e = key_expert(key);
         a.topk_idx[t * a.k + j] = e;
         a.topk_w[t * a.k + j] = p;   // scaled below, by this lane
-        ++counts[e];
+        atomicAdd(&counts[e], 1);
       }
     }
     const float scale = a.gate == LRM_GATE_TOPK ? 1.0f / chosen : inv;
@@ -169,13 +168,9 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void route_any(RouteArgs a) {
   __syncthreads();
   for (int e = threadIdx.x; e < a.pitch; e += kAnyWaves * kWave) {
     float p = 0.0f;
-    int c = 0;
-    for (int q = 0; q < kAnyWaves && e < E; ++q) {
-      p += shared[q * E + e];
-      c += ((int*)(shared + kAnyWaves * E))[q * E + e];
-    }
+    for (int q = 0; q < kAnyWaves && e < E; ++q) p += shared[q * E + e];
     a.part_prob[(int64_t)blockIdx.x * a.pitch + e] = p;
-    a.part_counts[(int64_t)blockIdx.x * a.pitch + e] = c;
+    a.part_counts[(int64_t)blockIdx.x * a.pitch + e] = e < E ? counts[e] : 0;
   }
   if (threadIdx.x == 0) {
     int n = 0, b = 0;
@@ -803,7 +798,7 @@ unsigned launch_rows_any(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
   if (a.k <= 16) return launch_rows_e<kBF16, 16>(a, o, s);
   // more choices than a lane's registers sort: a round of maxima per choice
   const unsigned nb = grid_for(((int64_t)a.T + kAnyWaves - 1) / kAnyWaves, kRouteBlocks);
-  hipLaunchKernelGGL(route_any<kBF16>, dim3(nb), dim3(kAnyWaves * kWave), (size_t)kAnyWaves * a.E * 8,
+  hipLaunchKernelGGL(route_any<kBF16>, dim3(nb), dim3(kAnyWaves * kWave), (size_t)(kAnyWaves + 1) * a.E * 4,
                      s, a);
   return nb;
 }

@@ -144,6 +144,16 @@ CASES = [
     dict(T=40, k=2, E=140, e_lo=0, E_loc=140, h=64, d=64),
     dict(T=17, k=8, E=1024, e_lo=0, E_loc=1024, h=32, d=16),
     dict(T=5, k=2, E=64, e_lo=32, E_loc=4, h=1032, d=1048),
+    # more units than workgroups, for every tile shape, with one, two and three steps of a unit (the
+    # loads run ahead over one unit's end, or over several units), and FC2's mirror images
+    dict(T=20000, k=1, E=2, e_lo=0, E_loc=2, h=8, d=1024),
+    dict(T=20000, k=1, E=2, e_lo=0, E_loc=2, h=1024, d=8),
+    dict(T=9000, k=2, E=70, e_lo=0, E_loc=70, h=136, d=512),
+    dict(T=8000, k=2, E=100, e_lo=0, E_loc=100, h=8, d=1024),
+    dict(T=8000, k=2, E=100, e_lo=0, E_loc=100, h=1024, d=72),
+    dict(T=3000, k=2, E=300, e_lo=0, E_loc=300, h=72, d=1024),
+    dict(T=3000, k=2, E=300, e_lo=0, E_loc=300, h=1032, d=16),
+    dict(T=100, k=1, E=2, e_lo=0, E_loc=2, h=8, d=8),
 ]
 IDS = ["T%dk%dE%d-%dh%dd%d" % (c["T"], c["k"], c["E"], c["E_loc"], c["h"], c["d"]) for c in CASES]
 
@@ -226,6 +236,37 @@ def test_bad_rows_are_reported():
     lrm.lrm_grouped_fc1_swiglu(c.P, rp, wild, c.x, c.W1, None, phi, c.ws)
     torch.cuda.synchronize()
     lrm.lrm_read_device_error(c.ws, clear=True)
+
+
+def test_padded_batch_through_the_sequences():
+    """Masked tokens take no expert: their outputs are the residual, their gradients and adot zeros;
+    the plan reports the pairs it left out and nothing else."""
+    import torch
+    from backward_token_expert_amd import lrm, path
+    T, k, E, h, d = 90, 2, 8, 64, 48
+    c = Case(T=T, k=k, E=E, e_lo=0, E_loc=E, h=h, d=d, dtype="f32", spare=0)
+    c.P = lrm.make_problem(T, k, E, 0, E, h, d, "f32", T * k, T * k)
+    router = lrm.make_router(T, E, k, "f32", "topk", 0.1)
+    rb, bufs = path.RouterBuffers(router), path.DeviceBuffers(c.P)
+    fwd, lay = path.ForwardBuffers(c.P), path.LayerBuffers(c.P)
+    rng = np.random.default_rng(13)
+    z, mask = rng.normal(size=(T, E)).astype(np.float32), rng.random(T) < 0.6
+    g = _dev(rng.normal(size=(T, h)).astype(np.float32))
+    full = lrm.make_policy(1)
+    x = c.x.clone()
+    x[_dev(~mask)] = float("nan")                  # padding may hold anything
+    path.route(router, _dev(z), rb, _dev(mask.astype(np.uint8)))
+    path.run_forward(c.P, full, rb.topk_idx, rb.topk_w, x, c.W1, c.W, bufs, fwd, c.res)
+    path.run(c.P, full, rb.topk_idx, rb.topk_w, g, fwd.phi, c.W, bufs)
+    path.run_layer(c.P, fwd.ac, x, c.W1, bufs, lay)
+    path.run_router_backward(c.P, router, _dev(z), bufs, rb)
+    assert lrm.lrm_read_device_error(bufs.ws) == 1   # EXPERT_ID
+    off = _dev(~mask)
+    assert int(bufs.cmp_off[-1]) == k * int(mask.sum()) == int(rb.counts.sum())
+    assert torch.equal(fwd.out[off], c.res[off]) and not lay.dx[off].any() and not rb.dlogits[off].any()
+    assert not rb.adot.reshape(T, k)[off].any()
+    for t in (fwd.out, lay.dx, lay.dW1, bufs.dW, rb.dlogits):
+        assert torch.isfinite(t).all()
 
 
 def layer_step(c, router, logits, rb, bufs, fwd, lay, clip, inp, policy, stream=None):

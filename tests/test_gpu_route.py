@@ -65,7 +65,8 @@ def check_route(rb, want, T):
 # may keep, the widest table, rows that are not 16-byte aligned, a large batch
 SHAPES = [(1, 128, 8), (1, 1, 1), (3, 5, 5), (64, 8, 2), (65, 7, 3), (333, 60, 6), (1021, 128, 8),
           (100, 131, 9), (77, 160, 6), (50, 256, 16), (40, 300, 40), (33, 512, 8), (20, 1000, 22),
-          (9, 2047, 4), (5, 4096, 12), (4096, 128, 8), (5000, 64, 4)]
+          (9, 2047, 4), (5, 4096, 12), (6, 4096, 40), (4096, 128, 8), (4097, 128, 2), (5000, 64, 4),
+          (9001, 128, 16), (2100, 250, 8)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
