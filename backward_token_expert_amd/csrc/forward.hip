@@ -92,6 +92,7 @@ struct FcArgs {
   void* out2;
   int32_t* err;
   int64_t units;   // the most units (row tile, column tile) there can be
+  bool skew;       // fc_bf16: units start at K steps of their own
 };
 
 // The token of pair p, or -1 for a pair id that is none.
@@ -102,6 +103,15 @@ __device__ __forceinline__ int64_t token_of(const FcArgs& g, int p) {
 // Operands are read through buffer resources: a row or chunk that is not there gets an offset beyond
 // the range and reads as zeros.
 constexpr uint32_t kOutOfRange = 0x80000000u;
+
+// The K step (of n) at which a unit of column block c of expert e starts; it takes the others in
+// turn, cyclically.  Units that all start at 0 read the same few hundred bytes of every weight row at
+// a time, and where the rows' pitch is a power of two those lie in a few of the memory's channels:
+// FC1 of 32 tokens (h 2048, d 768, 150 MB of weights in use) took 45.0 us so and takes 37.5.  A row's
+// sum depends on its expert and column alone, not on the batch around it.
+__device__ __forceinline__ int first_step(int c, int e, int n) {
+  return (int)((5u * (unsigned)c + 7u * (unsigned)e) % (unsigned)n);
+}
 
 // Buffer resource of 2^31 bytes from base: every offset that is used lies below what the host checked.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
@@ -270,6 +280,8 @@ struct Shape {
   static constexpr int T_BYTES = BT * ROW, W_BYTES = BW * ROW, STG = T_BYTES + W_BYTES;
   static constexpr int IT = T_BYTES / 1024 / NW, IW = W_BYTES / 1024 / NW, I = IT + IW;
   static_assert(IT * 1024 * NW == T_BYTES && IW * 1024 * NW == W_BYTES, "whole 1 KiB blocks a wave");
+  // may start units at any K step; tiles of many rows never do, and the code for it cost them 2 %
+  static constexpr bool SKEW = BT < 256;
   static constexpr int TABLE = 1024 + 1;                  // tiles before each expert
   // FC2's outputs go through 2 KiB of LDS a wavefront where as many workgroups still fit a CU.
   static constexpr int TABLE_BYTES = (TABLE + 3) / 4 * 16, OUT_BYTES = NW * 2048;
@@ -356,6 +368,7 @@ struct Loader {
   const char* pt;        // tokens and weights at k0
   const char* pw;
   int k0, wave, lane;
+  int nk, left;          // K steps of a unit, and those still to load
   bool more;             // a unit is left to load
 
   // the chunk that belongs at position l % 8 of row 8 q + l / 8
@@ -396,7 +409,11 @@ struct Loader {
     }
     pt = (const char*)g.A + (kSwiglu ? 0 : (int64_t)u.r0 * g.K * 2);
     pw = (const char*)g.B + (int64_t)u.e * (kSwiglu ? 2 : 1) * g.N * g.K * 2;
-    k0 = 0;
+    const int first = C::SKEW && g.skew ? first_step(u.n0 / (kSwiglu ? C::BW / 2 : C::BW), u.e, nk) : 0;
+    k0 = first * BK;
+    pt += first * C::ROW;
+    pw += first * C::ROW;
+    left = nk;
   }
 
   // Load q (tokens first) of the K step at k0 into the stage at LDS address `st`; where the step ends
@@ -423,6 +440,12 @@ struct Loader {
     pt += C::ROW;
     pw += C::ROW;
     k0 += BK;
+    --left;
+    if (C::SKEW && k0 >= nk * BK) {   // a skewed unit's first steps come last
+      k0 = 0;
+      pt -= nk * C::ROW;
+      pw -= nk * C::ROW;
+    }
   }
 };
 
@@ -575,6 +598,7 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
   ld.wave = wave;
   ld.lane = lane;
   const int nk = (g.K + BK - 1) / BK;
+  ld.nk = nk;
   Unit t = unit_of<C, kSwiglu>(g, before, row_tiles, cols, u), nx = t;
   int64_t un = u;        // the loader's unit
   ld.fetch(g, t);
@@ -585,7 +609,7 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
     if (ld.more) {
       ld.load_all(ring + s * C::STG, operand(ld.pt), operand(ld.pw), g.K);
       ld.step();
-      if (ld.k0 >= g.K) {
+      if (ld.left == 0) {
         un += nb;
         ld.more = un < hi;
         if (ld.more) {
@@ -626,13 +650,13 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of the stage are done
       lds_barrier();
       const uint32_t next = cur + C::STG == ring + C::S * C::STG ? ring : cur + C::STG;
-      if (ld.more && ld.k0 >= g.K) ld.begin(g, nx);
+      if (ld.more && ld.left == 0) ld.begin(g, nx);
       __builtin_amdgcn_sched_barrier(0);
       if (ld.more) {
         const __amdgpu_buffer_rsrc_t rt = operand(ld.pt), rw = operand(ld.pw);
         ld.load_all(cur, rt, rw, g.K);
         ld.step();
-        if (ld.k0 >= g.K) {   // the unit's last loads are out: its successor's rows
+        if (ld.left == 0) {   // the unit's last loads are out: its successor's rows
           un += nb;
           ld.more = un < hi;
           if (ld.more) {
@@ -788,24 +812,25 @@ __device__ __forceinline__ void few_tile(const FcArgs& g, const RowTile& t, int 
   for (int i = 0; i < WF; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  // whole 128-byte pieces of the rows, this wavefront's w, w + 4, ..; then the row's rest
+  // whole 128-byte pieces of the rows, this wavefront's w, w + 4, .. after a start that differs
+  // between workgroups; then the row's rest
   const int whole = g.K / STEP;
   FewPiece<TT> f[kFewAhead];
   if (whole > 0) {
+    const int first = first_step(n0 / (kSwiglu ? 16 : 32), t.e, whole);
+    const auto piece = [&](int c) {
+      const int at = (c < whole ? c : whole - 1) + first;
+      return (int64_t)(at < whole ? at : at - whole) * 128;
+    };
     // the loads run ahead without a condition, so that each wait is for one piece's loads alone;
     // past the end they fetch the last piece again
-    const int last = whole - 1;
 #pragma unroll
-    for (int q = 0; q < kFewAhead; ++q) {
-      const int c = w + q * kFewWaves;
-      f[q].load(pw, pt, (int64_t)(c < last ? c : last) * 128);
-    }
+    for (int q = 0; q < kFewAhead; ++q) f[q].load(pw, pt, piece(w + q * kFewWaves));
     for (int c = w; c < whole; c += kFewAhead * kFewWaves) {
 #pragma unroll
       for (int q = 0; q < kFewAhead; ++q) {
         if (c + q * kFewWaves < whole) f[q].template multiply<kBF16>(acc);
-        const int next = c + (kFewAhead + q) * kFewWaves;
-        f[q].load(pw, pt, (int64_t)(next < last ? next : last) * 128);
+        f[q].load(pw, pt, piece(c + (kFewAhead + q) * kFewWaves));
       }
     }
   }
@@ -896,19 +921,23 @@ constexpr int kDies = 8, kCUs = 256;
 
 // The bf16 tiles, by tokens x weight rows.  Measured over a whole layer of 128 experts (h 2048, d 768,
 // Zipf-skewed top-8 routing), us of FC1 / FC2 with Low, Mid, Big:
-//   256 tokens   67 / 35   85 / 41   80 / 57      (16 rows an expert on average)
-//   512          91 / 47   93 / 43  130 / 57      (32)
-//  2048         214 / 117 165 / 101 189 / 103     (128)
-//  4096         387 / 213 292 / 162 301 / 162     (256)
-// and over a 16-expert share (h 4096, d 1408) at 2048 tokens 598 / 310, 427 / 234, 361 / 218.
+//   256 tokens   60 / 35   71 / 40   72 / 56      (16 rows an expert on average)
+//   512          88 / 47   82 / 44  118 / 56      (32)
+//  2048         218 / 119 161 / 101 187 / 103     (128)
+//  4096         390 / 216 294 / 168 301 / 160     (256)
+// and over a 16-expert share (h 4096, d 1408) at 2048 tokens 611 / 320, 436 / 242, 379 / 221.
 using Low = Shape<2, 2, 2, 1, 3>;   // 64 x 128
 using Mid = Shape<4, 2, 2, 2, 3>;   // 128 x 256
 using Big = Shape<4, 2, 2, 4, 2>;   // 256 x 256
 constexpr int kMidRows = 24, kBigRows = 256;
-// Tokens up to which fc_few is the faster one: bf16 FC1 / FC2 of one token 16.7 / 9.0 against Low's
-// 18.1 / 10.5, of four 22.3 / 12.9 against 22.5 / 12.1; float32 (h = d = 512, 32 experts) 27 / 19 against
-// fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at 256.
-constexpr int kFewBF16 = 2, kFewF32 = 128;
+// Rows an expert below which units start at K steps of their own: with few rows the weights' way from
+// memory bounds the product (512 tokens of the layer above 82.2 us so, 86.1 without), with many the
+// units that share a panel should read it together (2048 tokens 173.9, 171.9).
+constexpr int kSkewRows = 64;
+// Tokens up to which fc_few is the faster one: bf16 FC1 / FC2 of one token 15.8 / 8.9 against Low's
+// 19.1 / 11.0, of two (h 4096, d 1408) 53.6 / 30.5 against 49.6 / 29.3; float32 (h = d = 512, 32 experts)
+// 27 / 19 against fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at 256.
+constexpr int kFewBF16 = 1, kFewF32 = 128;
 
 template <class C, bool kSwiglu>
 hipError_t launch_shape(const FcArgs& g, hipStream_t s) {
@@ -937,6 +966,7 @@ hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
     // share of a layer has capacity for every pair)
     const int64_t cap = (int64_t)p.L_cap / p.E_loc, most = 4 * ((int64_t)p.T * p.k / p.E);
     const int64_t rows = cap < most ? cap : most;
+    g.skew = rows < kSkewRows;
     if (rows >= kBigRows) return launch_shape<Big, kSwiglu>(g, s);
     if (rows >= kMidRows) return launch_shape<Mid, kSwiglu>(g, s);
     return launch_shape<Low, kSwiglu>(g, s);
