@@ -268,8 +268,8 @@ __device__ __forceinline__ void merge_lanes(double (&t)[KT]) {
   }
 }
 
-// exp(v - m) for v <= m by the hardware's power of two: the argument's rounding, (m - v) 2^-24, and
-// the instruction's own are each within what the products around it round.
+// exp(v - m) for v <= m by the hardware's power of two.  The argument's two roundings put it off by at
+// most 2 (m - v) 2^-24 of itself, and so by less than 2^-24 of the row's largest.
 __device__ __forceinline__ float exp_below(float v, float m) {
   return __builtin_amdgcn_exp2f((v - m) * 1.44269504f);
 }

@@ -334,7 +334,7 @@ def _arg(t, name, types, count, device, exact=False):
     if t is None or t.__class__ is int:
         return t
     n = t.numel()
-    if t.dtype in types and (n == count or n > count and not exact) and t.is_contiguous() and \
+    if (n == count or n > count and not exact) and t.dtype in types and t.is_contiguous() and \
             t.get_device() == device:
         return t.data_ptr()
     if t.dtype not in types:
@@ -372,8 +372,9 @@ def _elem(dtype):
 def _space(ws, device):
     if isinstance(ws, int):
         raise LrmError("ws: a tensor is needed, its size is part of the call")
-    n = ws.numel() * ws.element_size()
-    return _arg(ws, "ws", (ws.dtype,), 0, device), n
+    if ws.is_contiguous() and ws.get_device() == device:
+        return ws.data_ptr(), ws.nbytes
+    return _arg(ws, "ws", (ws.dtype,), 0, device), 0   # raises
 
 
 def make_router(T, E, k, dtype="f32", gate="topk", balance_coef=0.0) -> Router:
