@@ -477,6 +477,12 @@ __global__ __launch_bounds__(kFinalThreads) void route_final(const int32_t* __re
   const int tid = threadIdx.x, Q = pitch / 4, S = kFinalThreads / Q;   // pitch <= 4096
   const int slice = tid / Q, q = tid % Q;
   if (tid == 0) tokens = bits = 0;
+  int n = 0, bad = 0;
+  for (int b = tid; b < blocks; b += kFinalThreads) {
+    const int2 x = ((const int2*)part_tokens)[b];
+    n += x.x;
+    bad |= x.y;
+  }
   double p[4] = {0.0, 0.0, 0.0, 0.0};
   int c[4] = {0, 0, 0, 0};
   if (slice < S)
@@ -507,11 +513,6 @@ __global__ __launch_bounds__(kFinalThreads) void route_final(const int32_t* __re
     sc[tid][i] = c[i];
   }
   __syncthreads();
-  int n = 0, bad = 0;
-  for (int b = tid; b < blocks; b += kFinalThreads) {
-    n += part_tokens[2 * b];
-    bad |= part_tokens[2 * b + 1];
-  }
   n = wave_sum_int(n);
   bad = ballot(bad != 0) != 0 ? LRM_DEVERR_NONFINITE : 0;
   if (lane_id() == 0) {
@@ -524,6 +525,7 @@ __global__ __launch_bounds__(kFinalThreads) void route_final(const int32_t* __re
   for (int e = tid; e < E; e += kFinalThreads) {
     double x = 0.0;
     int y = 0;
+#pragma unroll 8
     for (int i = 0; i < S; ++i) {
       x += sp[i * Q + e / 4][e % 4];
       y += sc[i * Q + e / 4][e % 4];
@@ -783,7 +785,7 @@ constexpr int kShortBatch = 4096;   // tokens
 template <bool kBF16, int KT>
 unsigned launch_rows_e(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
   // few tokens: more lanes each, for the latency of one token's chain (one token 10.4 us with 4
-  // lanes, 7.3 with 8, 5.8 with 16); 32768 tokens take 21.8, 21.7 and 23.9 us
+  // lanes, 7.2 with 8, 5.8 with 16); 32768 tokens take 19.4 us with 8 and 21.9 with 16
   if (a.E <= 128 && a.T <= kShortBatch) return launch_rows<kBF16, 16, 8, KT, 8>(a, o, s);
   if (a.E <= 128) return launch_rows<kBF16, 8, 16, KT, 16>(a, o, s);
   if (a.E <= 256) return launch_rows<kBF16, 8, 32, KT, 8>(a, o, s);
