@@ -92,7 +92,6 @@ struct FcArgs {
   void* out2;
   int32_t* err;
   int64_t units;   // the most units (row tile, column tile) there can be
-  bool skew;       // fc_bf16: units start at K steps of their own
 };
 
 // The token of pair p, or -1 for a pair id that is none.
@@ -107,8 +106,9 @@ constexpr uint32_t kOutOfRange = 0x80000000u;
 // The K step (of n) at which a unit of column block c of expert e starts; it takes the others in
 // turn, cyclically.  Units that all start at 0 read the same few hundred bytes of every weight row at
 // a time, and where the rows' pitch is a power of two those lie in a few of the memory's channels:
-// FC1 of 32 tokens (h 2048, d 768, 150 MB of weights in use) took 45.0 us so and takes 37.5.  A row's
-// sum depends on its expert and column alone, not on the batch around it.
+// FC1 of 32 tokens (h 2048, d 768, 150 MB of weights in use) took 45.0 us so and takes 37.5 (34.0 with
+// the weights past the caches).  A row's sum depends on its expert and column alone, not on the batch
+// around it.
 __device__ __forceinline__ int first_step(int c, int e, int n) {
   return (int)((5u * (unsigned)c + 7u * (unsigned)e) % (unsigned)n);
 }
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kF32Threads, kLong ? 4 : 6) void fc_f32(FcArgs g) {
 constexpr int BK = 64;                                    // K step: rows of 128 bytes in LDS
 constexpr int CH = 8;                                     // their 16-byte chunks
 
-template <int WW_, int WT_, int MT_, int NT_, int S_>
+template <int WW_, int WT_, int MT_, int NT_, int S_, bool kSpread_ = false>
 struct Shape {
   static constexpr int WW = WW_, WT = WT_, MT = MT_, NT = NT_, S = S_;
   static constexpr int NW = WW * WT, THREADS = NW * kWave;
@@ -280,8 +280,9 @@ struct Shape {
   static constexpr int T_BYTES = BT * ROW, W_BYTES = BW * ROW, STG = T_BYTES + W_BYTES;
   static constexpr int IT = T_BYTES / 1024 / NW, IW = W_BYTES / 1024 / NW, I = IT + IW;
   static_assert(IT * 1024 * NW == T_BYTES && IW * 1024 * NW == W_BYTES, "whole 1 KiB blocks a wave");
-  // may start units at any K step; tiles of many rows never do, and the code for it cost them 2 %
-  static constexpr bool SKEW = BT < 256;
+  // For few rows an expert: units start at K steps of their own (see first_step), and the weights,
+  // of which a workgroup then reads every line alone, pass the caches by.
+  static constexpr bool SPREAD = kSpread_;
   static constexpr int TABLE = 1024 + 1;                  // tiles before each expert
   // FC2's outputs go through 2 KiB of LDS a wavefront where as many workgroups still fit a CU.
   static constexpr int TABLE_BYTES = (TABLE + 3) / 4 * 16, OUT_BYTES = NW * 2048;
@@ -294,11 +295,18 @@ struct Shape {
 
 // 16 bytes a lane from r + voff to LDS address lds + 16 lane.  Inline assembly, so that the compiler
 // does not wait for it before every LDS read; the pipeline orders it with vmcnt and barriers.
+template <bool kStream>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds), "v"(voff), "s"(r)
-               : "memory");
+  if constexpr (kStream)
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(r)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(r)
+                 : "memory");
 }
 
 template <int N>
@@ -409,7 +417,7 @@ struct Loader {
     }
     pt = (const char*)g.A + (kSwiglu ? 0 : (int64_t)u.r0 * g.K * 2);
     pw = (const char*)g.B + (int64_t)u.e * (kSwiglu ? 2 : 1) * g.N * g.K * 2;
-    const int first = C::SKEW && g.skew ? first_step(u.n0 / (kSwiglu ? C::BW / 2 : C::BW), u.e, nk) : 0;
+    const int first = C::SPREAD ? first_step(u.n0 / (kSwiglu ? C::BW / 2 : C::BW), u.e, nk) : 0;
     k0 = first * BK;
     pt += first * C::ROW;
     pw += first * C::ROW;
@@ -426,7 +434,7 @@ struct Loader {
     if constexpr (Q < C::IT) off = t[Q];
     else off = w[Q - C::IT];
     if (k0 + BK > K) off = k0 + chunk_of(q) * 8 < K ? off : kOutOfRange;
-    dma16(Q < C::IT ? rt : rw, st + (Q < C::IT ? 0 : C::T_BYTES) + q * 1024, off);
+    dma16<(C::SPREAD && Q >= C::IT)>(Q < C::IT ? rt : rw, st + (Q < C::IT ? 0 : C::T_BYTES) + q * 1024, off);
   }
   template <int Q = 0>
   __device__ __forceinline__ void load_all(uint32_t st, __amdgpu_buffer_rsrc_t rt, __amdgpu_buffer_rsrc_t rw,
@@ -441,7 +449,7 @@ struct Loader {
     pw += C::ROW;
     k0 += BK;
     --left;
-    if (C::SKEW && k0 >= nk * BK) {   // a skewed unit's first steps come last
+    if (C::SPREAD && k0 >= nk * BK) {   // a spread unit's first steps come last
       k0 = 0;
       pt -= nk * C::ROW;
       pw -= nk * C::ROW;
@@ -920,23 +928,23 @@ void launch_few(const lrm_problem& p, FcArgs g, hipStream_t s) {
 constexpr int kDies = 8, kCUs = 256;
 
 // The bf16 tiles, by tokens x weight rows.  Measured over a whole layer of 128 experts (h 2048, d 768,
-// Zipf-skewed top-8 routing), us of FC1 / FC2 with Low, Mid, Big:
-//   256 tokens   60 / 35   71 / 40   72 / 56      (16 rows an expert on average)
-//   512          88 / 47   82 / 44  118 / 56      (32)
-//  2048         218 / 119 161 / 101 187 / 103     (128)
-//  4096         390 / 216 294 / 168 301 / 160     (256)
-// and over a 16-expert share (h 4096, d 1408) at 2048 tokens 611 / 320, 436 / 242, 379 / 221.
-using Low = Shape<2, 2, 2, 1, 3>;   // 64 x 128
-using Mid = Shape<4, 2, 2, 2, 3>;   // 128 x 256
-using Big = Shape<4, 2, 2, 4, 2>;   // 256 x 256
-constexpr int kMidRows = 24, kBigRows = 256;
-// Rows an expert below which units start at K steps of their own: with few rows the weights' way from
-// memory bounds the product (512 tokens of the layer above 82.2 us so, 86.1 without), with many the
-// units that share a panel should read it together (2048 tokens 173.9, 171.9).
-constexpr int kSkewRows = 64;
-// Tokens up to which fc_few is the faster one: bf16 FC1 / FC2 of one token 15.8 / 8.9 against Low's
-// 19.1 / 11.0, of two (h 4096, d 1408) 53.6 / 30.5 against 49.6 / 29.3; float32 (h = d = 512, 32 experts)
-// 27 / 19 against fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at 256.
+// Zipf-skewed top-8 routing), us of FC1 / FC2 with Low, MidFew, Mid, Big:
+//   256 tokens   61 / 35   67 / 39   83 / 40   78 / 55      (16 rows an expert on average)
+//   512          96 / 51   81 / 43   90 / 43  124 / 55      (32)
+//  1024         150 / 78  120 / 66  123 / 63  126 / 78      (64)
+//  2048         271 / 142 168 / 105 164 / 103 185 / 104     (128)
+//  4096         533 / 271 312 / 177 288 / 167 301 / 162     (256)
+// and over a 16-expert share (h 4096, d 1408) at 256 tokens (64 rows) 148 / 72, 84 / 59, 101 / 62, 127 /
+// 57, at 2048 922 / 437, 437 / 245, 425 / 238, 367 / 218.
+using Low = Shape<2, 2, 2, 1, 3, true>;      // 64 x 128
+using MidFew = Shape<4, 2, 2, 2, 3, true>;   // 128 x 256
+using Mid = Shape<4, 2, 2, 2, 3>;
+using Big = Shape<4, 2, 2, 4, 2>;            // 256 x 256
+constexpr int kMidRows = 24, kSpreadRows = 96, kBigRows = 256;
+// Tokens up to which fc_few is the faster one: bf16 FC1 / FC2 of one token 18.3 / 8.9 against Low's
+// 21.4 / 11.9 (h 4096, d 1408: 40.7 / 22.5, 39.5 / 19.1), of two there 52.3 / 28.5 against 42.3 / 25.8;
+// float32 (h = d = 512, 32 experts) 27 / 19 against fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at
+// 256.
 constexpr int kFewBF16 = 1, kFewF32 = 128;
 
 template <class C, bool kSwiglu>
@@ -966,9 +974,9 @@ hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
     // share of a layer has capacity for every pair)
     const int64_t cap = (int64_t)p.L_cap / p.E_loc, most = 4 * ((int64_t)p.T * p.k / p.E);
     const int64_t rows = cap < most ? cap : most;
-    g.skew = rows < kSkewRows;
     if (rows >= kBigRows) return launch_shape<Big, kSwiglu>(g, s);
-    if (rows >= kMidRows) return launch_shape<Mid, kSwiglu>(g, s);
+    if (rows >= kSpreadRows) return launch_shape<Mid, kSwiglu>(g, s);
+    if (rows >= kMidRows) return launch_shape<MidFew, kSwiglu>(g, s);
     return launch_shape<Low, kSwiglu>(g, s);
   } else {
     const int bn = kSwiglu ? kBNH : 2 * kBNH;
