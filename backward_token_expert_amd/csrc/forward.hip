@@ -299,19 +299,21 @@ struct Shape {
 };
 
 // 16 bytes a lane from r + voff to LDS address lds + 16 lane.  Inline assembly, so that the compiler
-// does not wait for it before every LDS read; the pipeline orders it with vmcnt and barriers.
+// does not wait for it before every LDS read; the pipeline orders it with vmcnt and barriers.  The
+// s_nop is the wait state that a load into LDS needs behind a write of M0: within a statement the
+// compiler adds none.
 template <bool kStream>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t voff) {
   if constexpr (kStream)
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
                  :
                  : "s"(lds), "v"(voff), "s"(r)
-                 : "memory");
+                 : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(r)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 template <int N>

@@ -136,10 +136,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
 // and does not drain all outstanding loads before every LDS read; the pipeline below orders the
 // stages with explicit vmcnt waits and barriers instead.  M0 = lds + OFF (LDS byte address).  The
 // sum is formed outside the assembly: an s_add inside it would overwrite SCC, which the compiler
-// may hold live across the statement.
+// may hold live across the statement.  The s_nop is the wait state that a load into LDS needs behind
+// a write of M0: within a statement the compiler adds none.
 template <int OFF>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds + OFF), "v"(voff), "s"(r)
                : "memory", "m0");
