@@ -119,10 +119,14 @@ __device__ __forceinline__ int first_step(int c, int e, int n) {
 }
 
 // Buffer resource of 2^31 bytes from base: every offset that is used lies below what the host checked.
+// The base's words come from a vector instruction; a buffer access may read them five wait states
+// later, which the compiler does not keep for the accesses in assembly statements (dma16).  The s_nop
+// is that wait, and its outputs are what the loads read, so no vector instruction writes those again.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
   const uint64_t v = (uint64_t)(uintptr_t)base;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  asm("s_nop 4" : "+s"(lo), "+s"(hi));
   return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), (short)0,
                                            (int)kOutOfRange, 0x00020000);
 }

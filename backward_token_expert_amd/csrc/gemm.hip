@@ -119,17 +119,18 @@ constexpr uint32_t kOutOfRange = 0x80000000u;
 
 constexpr int64_t kMaxWindow = 0x7FFFFFF0;
 
-// A wave-uniform pointer, held in scalar registers.
-__device__ __forceinline__ const char* uniform(const char* p) {
-  const uint64_t v = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const char*)(uintptr_t)(((uint64_t)hi << 32) | lo);
-}
-
-// Buffer resource over [base, base + bytes), bytes in [0, kMaxWindow].
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+// Buffer resource over [base, base + bytes), bytes in [0, kMaxWindow], both uniform over the wave.
+// Its words come from vector instructions; a buffer access may read them five wait states later, which
+// the compiler does not keep for the accesses in assembly statements (dma16).  The s_nop is that wait,
+// and its outputs are what the loads read, so no vector instruction writes those again.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const char* base, int bytes) {
+  const uint64_t v = (uint64_t)(uintptr_t)base;
+  uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  bytes = __builtin_amdgcn_readfirstlane(bytes);
+  asm("s_nop 4" : "+s"(lo), "+s"(hi), "+s"(bytes));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), (short)0,
+                                           bytes, 0x00020000);
 }
 
 // The load is written as inline assembly: the compiler then does not track it as an LDS write
@@ -440,8 +441,8 @@ struct Loader {
 
   // wa / wb: LDS byte addresses of this wave's first 1 KiB block of the A / B part of the stage.
   __device__ __forceinline__ void fire(uint32_t wa, uint32_t wb) const {
-    const __amdgpu_buffer_rsrc_t r_a = make_rsrc(uniform(pa), __builtin_amdgcn_readfirstlane(na));
-    const __amdgpu_buffer_rsrc_t r_b = make_rsrc(uniform(pb), __builtin_amdgcn_readfirstlane(nb));
+    const __amdgpu_buffer_rsrc_t r_a = make_rsrc(pa, na);
+    const __amdgpu_buffer_rsrc_t r_b = make_rsrc(pb, nb);
     if (C::AKMN || k0 + kBK <= kend) {
       static_for<C::IA>([&](auto j) { dma16<decltype(j)::value * 1024>(r_a, wa, oa[decltype(j)::value]); });
     } else {

@@ -4,6 +4,7 @@ The compiler keeps them for the instructions it writes; an instruction inside an
 statement is hidden from it, and so is what such an instruction reads and writes.  liblrm.so's own
 code objects are disassembled and every path through them is walked backwards from
   - a load into LDS: one wait state after a scalar write of M0;
+  - a buffer or global access: five after a vector instruction wrote a scalar register it reads;
   - a DPP instruction: two after a vector instruction wrote the vector register it exchanges.
 An instruction is one wait state, s_nop N is N + 1.
 """
@@ -91,13 +92,19 @@ def m0_rule(ins):
         return nearest(ins, lambda o: o.op.startswith("s_") and o.args[:1] == ["m0"], 1)
 
 
+def scalar_rule(ins):
+    if ins.op.startswith(("buffer_", "global_", "scratch_", "flat_")):
+        used = frozenset().union(*[registers(a, "s") for a in ins.args])
+        return nearest(ins, lambda o: o.writes("s") & used, 5) if used else None
+
+
 def dpp_rule(ins):
     if ins.op.endswith("_dpp"):
         used = registers(ins.args[1], "v")
         return nearest(ins, lambda o: o.writes("v") & used, 2)
 
 
-RULES = {"m0": m0_rule, "dpp": dpp_rule}
+RULES = {"m0": m0_rule, "scalar": scalar_rule, "dpp": dpp_rule}
 
 
 def broken(text, rule):
@@ -106,9 +113,14 @@ def broken(text, rule):
 
 
 # What the check has to find, and to leave alone.
-WRONG = [("m0", "s_mov_b32 m0, s9\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
+WRONG = [("scalar", "v_readfirstlane_b32 s4, v0\n s_nop 3\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
+         ("scalar", "v_cmp_eq_u32_e64 s[6:7], v1, v2\n global_load_dword v1, v2, s[6:7]"),
+         ("m0", "s_mov_b32 m0, s9\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
          ("dpp", "v_max_f64 v[2:3], v[4:5], v[6:7]\n s_nop 0\n v_mov_b32_dpp v9, v3 quad_perm:[1,0,3,2]")]
-RIGHT = [("m0", "s_mov_b32 m0, s9\n s_nop 0\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
+RIGHT = [("scalar", "v_readfirstlane_b32 s4, v0\n s_nop 4\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
+         ("scalar", "s_mov_b32 s4, s9\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
+         ("scalar", "v_readfirstlane_b32 s8, v0\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
+         ("m0", "s_mov_b32 m0, s9\n s_nop 0\n buffer_load_dwordx4 v1, s[4:7], 0 offen lds"),
          ("m0", "s_mov_b32 m0, s9\n buffer_load_dwordx4 v[0:3], v1, s[4:7], 0 offen"),
          ("dpp", "v_max_f64 v[2:3], v[4:5], v[6:7]\n s_nop 1\n v_mov_b32_dpp v9, v3 quad_perm:[1,0,3,2]"),
          ("dpp", "v_max_f64 v[2:3], v[4:5], v[6:7]\n v_mov_b32_dpp v9, v4 quad_perm:[1,0,3,2]")]
