@@ -68,6 +68,15 @@ lrm_status check_router(const lrm_router* r) {
   return LRM_OK;
 }
 
+// A problem of the forward calls and lrm_gate_dots, whose capacities may be 0: a share without rows.
+lrm_status check_forward_problem(const lrm_problem* p) {
+  if (!p) return LRM_ERR_INVALID_ARGUMENT;
+  lrm_problem q = *p;
+  q.L_cap += q.L_cap == 0;
+  q.K_cap += q.K_cap == 0;
+  return check_problem(&q);
+}
+
 lrm_status check_forward_ws(const lrm_problem* p, const void* ws, size_t ws_bytes) {
   if (!ws) return LRM_ERR_INVALID_ARGUMENT;
   if (!aligned16(ws)) return LRM_ERR_UNSUPPORTED;
@@ -409,8 +418,9 @@ lrm_status lrm_route_backward(const lrm_router* router, const void* logits,
 lrm_status lrm_gate_dots(const lrm_problem* problem, const int32_t* sel_pair,
                          const int32_t* cmp_off, const float* dphi, const void* Phic, float* adot,
                          void* ws, size_t ws_bytes, hipStream_t stream) {
-  LRM_TRY(check_problem(problem));
-  if (!sel_pair || !cmp_off || !dphi || !Phic || !adot) return LRM_ERR_INVALID_ARGUMENT;
+  LRM_TRY(check_forward_problem(problem));
+  if (!cmp_off || !adot) return LRM_ERR_INVALID_ARGUMENT;
+  if (problem->K_cap > 0 && (!sel_pair || !dphi || !Phic)) return LRM_ERR_INVALID_ARGUMENT;
   if (!aligned16(dphi) || !aligned16(Phic)) return LRM_ERR_UNSUPPORTED;
   LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
   return from_hip(lrm::launch_gate_dots(*problem, sel_pair, cmp_off, dphi, Phic, adot, (char*)ws,
@@ -418,14 +428,15 @@ lrm_status lrm_gate_dots(const lrm_problem* problem, const int32_t* sel_pair,
 }
 
 size_t lrm_forward_workspace_bytes(const lrm_problem* problem) {
-  return check_problem(problem) == LRM_OK ? lrm::forward_ws_bytes(*problem) : 0;
+  return check_forward_problem(problem) == LRM_OK ? lrm::forward_ws_bytes(*problem) : 0;
 }
 
 lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row_pair,
                                   const int32_t* fwd_off, const void* x, const void* W1, void* ac,
                                   void* phi, void* ws, size_t ws_bytes, hipStream_t stream) {
-  LRM_TRY(check_problem(problem));
-  if (!row_pair || !fwd_off || !x || !W1 || !phi) return LRM_ERR_INVALID_ARGUMENT;
+  LRM_TRY(check_forward_problem(problem));
+  if (!fwd_off || !x || !W1) return LRM_ERR_INVALID_ARGUMENT;
+  if (problem->L_cap > 0 && (!row_pair || !phi)) return LRM_ERR_INVALID_ARGUMENT;
   if (!aligned16(x) || !aligned16(W1) || !aligned16(ac) || !aligned16(phi)) return LRM_ERR_UNSUPPORTED;
   const int64_t row = problem->h * element_bytes(problem->dtype);
   if (problem->T * row > kMaxOperand || 2 * problem->d * row > kMaxOperand) return LRM_ERR_UNSUPPORTED;
@@ -436,8 +447,9 @@ lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row
 
 lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
                            const void* W, void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
-  LRM_TRY(check_problem(problem));
-  if (!fwd_off || !phi || !W || !y) return LRM_ERR_INVALID_ARGUMENT;
+  LRM_TRY(check_forward_problem(problem));
+  if (!fwd_off || !W) return LRM_ERR_INVALID_ARGUMENT;
+  if (problem->L_cap > 0 && (!phi || !y)) return LRM_ERR_INVALID_ARGUMENT;
   if (!aligned16(phi) || !aligned16(W) || !aligned16(y)) return LRM_ERR_UNSUPPORTED;
   // one expert's weights, and the 256 rows of phi of a tile
   const int64_t row = problem->d * element_bytes(problem->dtype);
@@ -450,8 +462,9 @@ lrm_status lrm_combine_tokens(const lrm_problem* problem, const int32_t* row_pai
                               const int32_t* fwd_off, const float* topk_w, const void* y,
                               const void* residual, void* out, void* ws, size_t ws_bytes,
                               hipStream_t stream) {
-  LRM_TRY(check_problem(problem));
-  if (!row_pair || !fwd_off || !topk_w || !y || !out) return LRM_ERR_INVALID_ARGUMENT;
+  LRM_TRY(check_forward_problem(problem));
+  if (!fwd_off || !topk_w || !out) return LRM_ERR_INVALID_ARGUMENT;
+  if (problem->L_cap > 0 && (!row_pair || !y)) return LRM_ERR_INVALID_ARGUMENT;
   if (!aligned16(y) || !aligned16(residual) || !aligned16(out)) return LRM_ERR_UNSUPPORTED;
   LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
   return from_hip(lrm::launch_combine(*problem, row_pair, fwd_off, topk_w, y, residual, out,

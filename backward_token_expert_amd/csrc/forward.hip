@@ -967,6 +967,7 @@ hipError_t launch_shape(const FcArgs& g, hipStream_t s) {
 
 template <bool kBF16, bool kSwiglu>
 hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
+  if (p.L_cap == 0) return hipSuccess;   // no row
   if (p.T <= (kBF16 ? kFewBF16 : kFewF32)) {   // an expert is chosen once a token: T rows at most
     if constexpr (kBF16) {
       launch_few<kBF16, kSwiglu, 1>(p, g, s);
@@ -1173,7 +1174,7 @@ void launch_combine_t(const lrm_problem& p, const int32_t* row_pair, const int32
     return;
   }
   const int64_t lb = ((int64_t)p.L_cap + kBlock - 1) / kBlock;
-  hipLaunchKernelGGL(forward_rows, dim3((unsigned)(lb < 2048 ? lb : 2048)), dim3(kBlock), 0, s,
+  hipLaunchKernelGGL(forward_rows, dim3((unsigned)(lb < 1 ? 1 : (lb < 2048 ? lb : 2048))), dim3(kBlock), 0, s,
                      row_pair, fwd_off, p.E_loc, p.L_cap, (int64_t)p.T * p.k, map, err);
   launch_tokens<kBF16, false, 4, 2>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
 }

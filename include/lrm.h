@@ -475,6 +475,8 @@ lrm_status lrm_scatter_tokens(const lrm_problem* problem, const int32_t* sel_pai
  *    lrm_forward_workspace_bytes only (lrm_workspace_bytes of the same problem is always
  *    enough, so a training step may pass the one it has).  They may overwrite all of those bytes
  *    but the error word, so not between lrm_score_norms and lrm_score_combine on one workspace.
+ *  - In those four calls L_cap and K_cap may be 0 (a share without a row); the arrays of rows, which
+ *    are empty then, may be NULL.
  *  - Two calls that may run at the same time need a workspace each.
  * ------------------------------------------------------------------------------------------------ */
 
