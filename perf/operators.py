@@ -292,8 +292,7 @@ def _plain_clip(s):
 def _problem(s):
     from backward_token_expert_amd import lrm
     c = s["case"]
-    # a capacity is at least one row
-    rows = max(1, s["sel_pair"].numel() if c["op"] == "router_grad" else s["row_pair"].numel())
+    rows = s["sel_pair"].numel() if c["op"] == "router_grad" else s["row_pair"].numel()
     return lrm.make_problem(c["T"], c["k"], c["E"], 0, c["E_loc"], c.get("h", 8), c["d"],
                             c["dtype"], rows, rows)
 
@@ -320,11 +319,7 @@ def _own_router_grad(s):
         s["ws"] = torch.zeros(lrm.lrm_forward_workspace_bytes(s["problem"]), dtype=torch.uint8, device=DEV)
         s["adot"] = torch.empty(c["T"] * c["k"], device=DEV)
         s["dlogits"] = torch.empty(c["T"], c["E"], device=DEV)
-        # for a step that keeps no row: buffers of the one-row capacity, which cmp_off leaves unread
-        s["none"] = [torch.zeros(1, *s[n].shape[1:], dtype=s[n].dtype, device=DEV)
-                     for n in ("sel_pair", "dphi", "Phic")]
-    sel_pair, dphi, Phic = (s["sel_pair"], s["dphi"], s["Phic"]) if s["sel_pair"].numel() else s["none"]
-    lrm.lrm_gate_dots(s["problem"], sel_pair, s["cmp_off"], dphi, Phic, s["adot"], s["ws"])
+    lrm.lrm_gate_dots(s["problem"], s["sel_pair"], s["cmp_off"], s["dphi"], s["Phic"], s["adot"], s["ws"])
     lrm.lrm_route_backward(s["router"], s["logits"], s["topk_idx"], s["topk_w"], s["counts"],
                            s["adot"], s["dlogits"])
     return {"adot": s["adot"], "dlogits": s["dlogits"]}
