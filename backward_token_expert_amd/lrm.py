@@ -465,7 +465,8 @@ class TensorList:
     once and used for every step; it keeps the tensors alive."""
 
     def __init__(self, src, dst):
-        self.src, self.dst = list(src), list(src if dst is None else dst)
+        self.src = list(src)
+        self.dst = list(self.src if dst is None else dst)
         if len(self.src) != len(self.dst):
             raise LrmError(f"{len(self.src)} sources, {len(self.dst)} destinations")
         self.n = len(self.src)
