@@ -5,8 +5,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <new>
-#include <vector>
 
 #include "lrm_forward.hpp"
 #include "lrm_internal.hpp"
@@ -88,8 +86,58 @@ int64_t element_bytes(int32_t dtype) { return dtype == LRM_BF16 ? 2 : 4; }
 // Largest operand the forward products address with 32-bit byte offsets.
 constexpr int64_t kMaxOperand = (int64_t)1 << 31;
 
-// The list's entries are well formed; with `write`, also that no element is written by one entry
-// and read or written by another, nor by an entry whose dst overlaps its src without being it.
+// Where an entry of a tensor list writes (id = 2 * its index) or reads (2 * index + 1).
+struct Start {
+  uintptr_t at;
+  int64_t id;
+};
+
+bool before(const Start& a, const Start& b) { return a.at != b.at ? a.at < b.at : a.id < b.id; }
+
+// Whether some element is written by one entry and read or written by another, or by an entry whose
+// dst overlaps its src without being it.  The ranges are looked at in order of their starts: one
+// overlaps an earlier one if it starts before that one's end.  The library allocates nothing, so each
+// pass over the list takes the lowest starts that are left, kKeep to 2 kKeep of them, and sorts those: a
+// list of 40 takes 2 us on the host, one of 1000 25 to 100 (one pass), one of 10000 0.5 to 3 ms (ten).
+bool overlapping(const lrm_tensor* list, int32_t n) {
+  constexpr int kKeep = 1024;
+  Start batch[2 * kKeep], last{}, limit{};
+  uintptr_t end = 0, written_end = 0;
+  for (bool first = true, more = true; more; first = false) {
+    int m = 0;
+    more = false;   // starts beyond `limit`, the highest that is kept, are left for a later pass
+    const auto take = [&](const void* p, int64_t id) {
+      const Start r{(uintptr_t)p, id};
+      if ((!first && !before(last, r)) || (more && before(limit, r))) return;
+      if (m == 2 * kKeep) {
+        std::nth_element(batch, batch + kKeep - 1, batch + m, before);
+        limit = batch[kKeep - 1];
+        m = kKeep;
+        more = true;
+        if (before(limit, r)) return;
+      }
+      batch[m++] = r;
+    };
+    for (int32_t i = 0; i < n; ++i) {
+      if (list[i].count == 0) continue;
+      take(list[i].dst, 2 * (int64_t)i);
+      if (list[i].src != list[i].dst) take(list[i].src, 2 * (int64_t)i + 1);
+    }
+    std::sort(batch, batch + m, before);
+    for (int i = 0; i < m; ++i) {
+      const lrm_tensor& t = list[batch[i].id / 2];
+      const uintptr_t lo = batch[i].at, hi = lo + (uintptr_t)(t.count * element_bytes(t.dtype));
+      const bool written = batch[i].id % 2 == 0;
+      if (lo < written_end || (written && lo < end)) return true;
+      end = std::max(end, hi);
+      if (written) written_end = std::max(written_end, hi);
+    }
+    if (m > 0) last = batch[m - 1];
+  }
+  return false;
+}
+
+// The list's entries are well formed; with `write`, also that they do not overlap.
 lrm_status check_tensors(const lrm_tensor* list, int32_t n, bool write) {
   if (n < 0 || (n > 0 && !list)) return LRM_ERR_INVALID_ARGUMENT;
   int64_t total = 0;
@@ -104,33 +152,7 @@ lrm_status check_tensors(const lrm_tensor* list, int32_t n, bool write) {
     if (!t.src || (write && !t.dst)) return LRM_ERR_INVALID_ARGUMENT;
     if (((uintptr_t)t.src & e) || (write && ((uintptr_t)t.dst & e))) return LRM_ERR_UNSUPPORTED;
   }
-  if (!write) return LRM_OK;
-  struct Range {
-    uintptr_t lo, hi;
-    bool written;
-  };
-  std::vector<Range> ranges;
-  try {
-    ranges.reserve(2 * (size_t)n);
-  } catch (const std::bad_alloc&) {
-    return LRM_ERR_UNSUPPORTED;
-  }
-  for (int32_t i = 0; i < n; ++i) {
-    const lrm_tensor& t = list[i];
-    if (t.count == 0) continue;
-    const uintptr_t bytes = (uintptr_t)(t.count * element_bytes(t.dtype));
-    ranges.push_back({(uintptr_t)t.dst, (uintptr_t)t.dst + bytes, true});
-    if (t.src != t.dst) ranges.push_back({(uintptr_t)t.src, (uintptr_t)t.src + bytes, false});
-  }
-  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  // in order of their starts: a range overlaps an earlier one if it starts before that one's end
-  uintptr_t end = 0, written_end = 0;
-  for (const Range& r : ranges) {
-    if (r.lo < written_end || (r.written && r.lo < end)) return LRM_ERR_INVALID_ARGUMENT;
-    end = std::max(end, r.hi);
-    if (r.written) written_end = std::max(written_end, r.hi);
-  }
-  return LRM_OK;
+  return write && overlapping(list, n) ? LRM_ERR_INVALID_ARGUMENT : LRM_OK;
 }
 
 lrm_status check_grad_ws(int32_t n, const void* ws, size_t ws_bytes) {
