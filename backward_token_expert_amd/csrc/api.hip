@@ -169,6 +169,36 @@ lrm_status check_grad_ws(int32_t n, const void* ws, size_t ws_bytes) {
     if (_s != LRM_OK) return _s;       \
   } while (0)
 
+namespace {
+
+// lrm_grouped_fc2 and lrm_combine_tokens; `wide`: y in float32 whatever the layer's type.
+lrm_status fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi, const void* W,
+               void* y, bool wide, void* ws, size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_forward_problem(problem));
+  if (!fwd_off || !W) return LRM_ERR_INVALID_ARGUMENT;
+  if (problem->L_cap > 0 && (!phi || !y)) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(phi) || !aligned16(W) || !aligned16(y)) return LRM_ERR_UNSUPPORTED;
+  // one expert's weights, and the 256 rows of phi of a tile
+  const int64_t row = problem->d * element_bytes(problem->dtype);
+  if (problem->h * row > kMaxOperand || 256 * row > kMaxOperand) return LRM_ERR_UNSUPPORTED;
+  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
+  return from_hip(lrm::launch_fc2(*problem, fwd_off, phi, W, y, wide, stream));
+}
+
+lrm_status combine(const lrm_problem* problem, const int32_t* row_pair, const int32_t* fwd_off,
+                   const float* topk_w, const void* y, bool wide, const void* residual, void* out,
+                   void* ws, size_t ws_bytes, hipStream_t stream) {
+  LRM_TRY(check_forward_problem(problem));
+  if (!fwd_off || !topk_w || !out) return LRM_ERR_INVALID_ARGUMENT;
+  if (problem->L_cap > 0 && (!row_pair || !y)) return LRM_ERR_INVALID_ARGUMENT;
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(out)) return LRM_ERR_UNSUPPORTED;
+  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
+  return from_hip(lrm::launch_combine(*problem, row_pair, fwd_off, topk_w, y, wide, residual, out,
+                                      (char*)ws, stream));
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t lrm_workspace_bytes(const lrm_problem* problem) {
@@ -469,28 +499,27 @@ lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row
 
 lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
                            const void* W, void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
-  LRM_TRY(check_forward_problem(problem));
-  if (!fwd_off || !W) return LRM_ERR_INVALID_ARGUMENT;
-  if (problem->L_cap > 0 && (!phi || !y)) return LRM_ERR_INVALID_ARGUMENT;
-  if (!aligned16(phi) || !aligned16(W) || !aligned16(y)) return LRM_ERR_UNSUPPORTED;
-  // one expert's weights, and the 256 rows of phi of a tile
-  const int64_t row = problem->d * element_bytes(problem->dtype);
-  if (problem->h * row > kMaxOperand || 256 * row > kMaxOperand) return LRM_ERR_UNSUPPORTED;
-  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
-  return from_hip(lrm::launch_fc2(*problem, fwd_off, phi, W, y, stream));
+  return fc2(problem, fwd_off, phi, W, y, false, ws, ws_bytes, stream);
+}
+
+lrm_status lrm_grouped_fc2_wide(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
+                                const void* W, float* y, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  return fc2(problem, fwd_off, phi, W, y, true, ws, ws_bytes, stream);
 }
 
 lrm_status lrm_combine_tokens(const lrm_problem* problem, const int32_t* row_pair,
                               const int32_t* fwd_off, const float* topk_w, const void* y,
                               const void* residual, void* out, void* ws, size_t ws_bytes,
                               hipStream_t stream) {
-  LRM_TRY(check_forward_problem(problem));
-  if (!fwd_off || !topk_w || !out) return LRM_ERR_INVALID_ARGUMENT;
-  if (problem->L_cap > 0 && (!row_pair || !y)) return LRM_ERR_INVALID_ARGUMENT;
-  if (!aligned16(y) || !aligned16(residual) || !aligned16(out)) return LRM_ERR_UNSUPPORTED;
-  LRM_TRY(check_forward_ws(problem, ws, ws_bytes));
-  return from_hip(lrm::launch_combine(*problem, row_pair, fwd_off, topk_w, y, residual, out,
-                                      (char*)ws, stream));
+  return combine(problem, row_pair, fwd_off, topk_w, y, false, residual, out, ws, ws_bytes, stream);
+}
+
+lrm_status lrm_combine_tokens_wide(const lrm_problem* problem, const int32_t* row_pair,
+                                   const int32_t* fwd_off, const float* topk_w, const float* y,
+                                   const void* residual, void* out, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  return combine(problem, row_pair, fwd_off, topk_w, y, true, residual, out, ws, ws_bytes, stream);
 }
 
 size_t lrm_grad_workspace_bytes(const lrm_tensor* list, int32_t n) {

@@ -8,8 +8,10 @@
 //
 // Products, activation and the sum over a token's rows are float32; ac, phi, y and out are rounded to
 // the layer's type where they are stored.  ac and phi are what the backward takes in that type.  y in
-// it halves the bytes of its way through memory (1 GB each way in the Qwen3 share, 200 of 1040 us), for
-// one rounding more: sqrt(2) times the error of out's own.
+// it halves the bytes of its way through memory, and adds sum_p |alpha_p| 2^-8 |y_p| to out's own error of
+// 2^-8 |out|: more than that where a token's terms cancel.  A caller who does not want it gives float32
+// rows (kWide).  Qwen3 share with the residual, bf16 / float32 rows: FC2 810-850 / 1030 us, combine 227 /
+// 486, out against 64 bits 1.76e-3 / 1.66e-3 of its norm; one token: no difference in time.
 #include <math.h>
 
 #include "lrm_device.hpp"
@@ -544,7 +546,22 @@ __device__ __forceinline__ void store_direct(const uint4 (&q)[n][2], uint16_t* o
     }
 }
 
-// The same two tiles through `stage` (2 KiB of LDS, this wavefront's), 16 tokens at a time: an
+// Two unrounded 32-column tiles of 32 tokens to float32 rows, from where the lanes hold them.
+__device__ __forceinline__ void store_wide(const f32x16& a, const f32x16& b, float* out, int64_t pitch,
+                                           int64_t r0, int64_t r1, int col, int end, int lane) {
+  const int64_t r = r0 + (lane & 31);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = col + 32 * i + 8 * q + 4 * (lane >> 5);
+      const f32x16& v = i ? b : a;
+      if (r < r1 && c < end)
+        *(float4*)(out + r * pitch + c) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+}
+
+// Two packed tiles (see store_direct) through `stage` (2 KiB of LDS, this wavefront's), 16 tokens at a time: an
 // instruction writes 8 rows by 128 bytes.  FC2's outputs are 20 % of its time (a copy that stores
 // nothing takes 673 us where the Qwen3 share takes 840 to 868); this saves 3 % of it.  FC1's, whose two
 // halves and phi come in runs of 64 bytes a wavefront, were no faster this way.
@@ -573,7 +590,7 @@ __device__ __forceinline__ void store_staged(const uint4 (&q)[2][2], uint16_t* o
   }
 }
 
-template <class C, bool kSwiglu>
+template <class C, bool kSwiglu, bool kWide>
 __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   int* before = (int*)(lds + C::S * C::STG);
@@ -712,6 +729,8 @@ __global__ __launch_bounds__(C::THREADS) void fc_bf16(FcArgs g, int nxcd) {
         for (int k = 0; k < 16; ++k) v[k] = silu_mul_fast(acc[0][j][k], acc[1][j][k]);
         pack_tile(v, q[0]);
         store_direct<1>(q, (uint16_t*)g.out2, g.N, r0, t.r1, col, g.N, lane);
+      } else if constexpr (kWide) {
+        store_wide(acc[0][j], acc[1][j], (float*)g.out, g.N, r0, t.r1, t.n0 + ww * 64, g.N, lane);
       } else {
         uint4 q[2][2];
 #pragma unroll
@@ -802,7 +821,7 @@ struct FewPiece {
 };
 
 // One tile with TT token operands.
-template <bool kBF16, bool kSwiglu, int TT>
+template <bool kBF16, bool kSwiglu, bool kWide, int TT>
 __device__ __forceinline__ void few_tile(const FcArgs& g, const RowTile& t, int n0, int64_t u,
                                          f32x4 (*part)[kWave]) {
   constexpr int ESZ = kBF16 ? 2 : 4, V = 16 / ESZ;
@@ -893,7 +912,7 @@ __device__ __forceinline__ void few_tile(const FcArgs& g, const RowTile& t, int 
           }
           store_elem<kBF16>(g.out2, r * g.N + c, silu_mul(v[i], x[i]));
         } else {
-          store_elem<kBF16>(g.out, r * g.N + c, v[i]);
+          store_elem<kBF16 && !kWide>(g.out, r * g.N + c, v[i]);
         }
       }
     }
@@ -901,7 +920,7 @@ __device__ __forceinline__ void few_tile(const FcArgs& g, const RowTile& t, int 
   __syncthreads();
 }
 
-template <bool kBF16, bool kSwiglu, int TT>
+template <bool kBF16, bool kSwiglu, bool kWide, int TT>
 __global__ __launch_bounds__(kFewWaves * kWave) void fc_few(FcArgs g) {
   constexpr int BN = kSwiglu ? 16 : 32;        // output columns
   __shared__ f32x4 part[kFewWaves * WF * TT][kWave];
@@ -912,11 +931,11 @@ __global__ __launch_bounds__(kFewWaves * kWave) void fc_few(FcArgs g) {
     const int n0 = (int)(u % cols) * BN, rows = t.r1 - t.r0;
     // as many token operands as the tile's rows need
     if (TT > 2 && rows > 32)
-      few_tile<kBF16, kSwiglu, TT>(g, t, n0, u, part);
+      few_tile<kBF16, kSwiglu, kWide, TT>(g, t, n0, u, part);
     else if (TT > 1 && rows > 16)
-      few_tile<kBF16, kSwiglu, 2>(g, t, n0, u, part);
+      few_tile<kBF16, kSwiglu, kWide, 2>(g, t, n0, u, part);
     else
-      few_tile<kBF16, kSwiglu, 1>(g, t, n0, u, part);
+      few_tile<kBF16, kSwiglu, kWide, 1>(g, t, n0, u, part);
   }
 }
 
@@ -928,11 +947,11 @@ inline int64_t most_tiles(const lrm_problem& p, int bm) {
 
 inline unsigned grid_of(int64_t units) { return (unsigned)(units < (1 << 20) ? units : 1 << 20); }
 
-template <bool kBF16, bool kSwiglu, int TT>
+template <bool kBF16, bool kSwiglu, bool kWide, int TT>
 void launch_few(const lrm_problem& p, FcArgs g, hipStream_t s) {
   const int bn = kSwiglu ? 16 : 32;
   g.units = most_tiles(p, 16 * TT) * ((g.N + bn - 1) / bn);
-  hipLaunchKernelGGL((fc_few<kBF16, kSwiglu, TT>), dim3(grid_of(g.units)), dim3(kFewWaves * kWave), 0, s, g);
+  hipLaunchKernelGGL((fc_few<kBF16, kSwiglu, kWide, TT>), dim3(grid_of(g.units)), dim3(kFewWaves * kWave), 0, s, g);
 }
 
 // Workgroups of the persistent products: one a CU, a multiple of the dies.
@@ -958,26 +977,27 @@ constexpr int kMidRows = 24, kSpreadRows = 96, kBigRows = 256;
 // 256.
 constexpr int kFewBF16 = 1, kFewF32 = 128;
 
-template <class C, bool kSwiglu>
+template <class C, bool kSwiglu, bool kWide>
 hipError_t launch_shape(const FcArgs& g, hipStream_t s) {
   constexpr int per_cu = 160 * 1024 / C::LDS;
-  hipLaunchKernelGGL((fc_bf16<C, kSwiglu>), dim3(kCUs * per_cu), dim3(C::THREADS), 0, s, g, kDies);
+  hipLaunchKernelGGL((fc_bf16<C, kSwiglu, kWide>), dim3(kCUs * per_cu), dim3(C::THREADS), 0, s, g, kDies);
   return hipGetLastError();
 }
 
-template <bool kBF16, bool kSwiglu>
+// kWide: a bf16 layer's y in float32.
+template <bool kBF16, bool kSwiglu, bool kWide = false>
 hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
   if (p.L_cap == 0) return hipSuccess;   // no row
   if (p.T <= (kBF16 ? kFewBF16 : kFewF32)) {   // an expert is chosen once a token: T rows at most
     if constexpr (kBF16) {
-      launch_few<kBF16, kSwiglu, 1>(p, g, s);
+      launch_few<kBF16, kSwiglu, kWide, 1>(p, g, s);
     } else {
       if (p.T <= 16)
-        launch_few<kBF16, kSwiglu, 1>(p, g, s);
+        launch_few<kBF16, kSwiglu, kWide, 1>(p, g, s);
       else if (p.T <= 32)
-        launch_few<kBF16, kSwiglu, 2>(p, g, s);
+        launch_few<kBF16, kSwiglu, kWide, 2>(p, g, s);
       else
-        launch_few<kBF16, kSwiglu, 4>(p, g, s);
+        launch_few<kBF16, kSwiglu, kWide, 4>(p, g, s);
     }
     return hipGetLastError();
   }
@@ -986,10 +1006,10 @@ hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
     // share of a layer has capacity for every pair)
     const int64_t cap = (int64_t)p.L_cap / p.E_loc, most = 4 * ((int64_t)p.T * p.k / p.E);
     const int64_t rows = cap < most ? cap : most;
-    if (rows >= kBigRows) return launch_shape<Big, kSwiglu>(g, s);
-    if (rows >= kSpreadRows) return launch_shape<Mid, kSwiglu>(g, s);
-    if (rows >= kMidRows) return launch_shape<MidFew, kSwiglu>(g, s);
-    return launch_shape<Low, kSwiglu>(g, s);
+    if (rows >= kBigRows) return launch_shape<Big, kSwiglu, kWide>(g, s);
+    if (rows >= kSpreadRows) return launch_shape<Mid, kSwiglu, kWide>(g, s);
+    if (rows >= kMidRows) return launch_shape<MidFew, kSwiglu, kWide>(g, s);
+    return launch_shape<Low, kSwiglu, kWide>(g, s);
   } else {
     const int bn = kSwiglu ? kBNH : 2 * kBNH;
     g.units = most_tiles(p, kBM) * ((g.N + bn - 1) / bn);
@@ -1044,6 +1064,28 @@ struct Chunk<false> {
   }
 };
 
+// The part of a row of y under one such chunk, in y's type: 16 bytes, or for a bf16 layer's float32 rows
+// (kWide) 32.
+template <bool kBF16, bool kWide>
+struct RowPart {
+  using C = Chunk<kBF16 && !kWide>;
+  static constexpr int N = kWide ? 2 : 1;
+  uint4 q[N];
+  __device__ __forceinline__ void load(const uint4* row, int ch, bool in) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = in ? load_nt(row + ch * N + i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void add(float w, float (&acc)[N * C::V]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[C::V];
+      C::get(q[i], v);
+#pragma unroll
+      for (int j = 0; j < C::V; ++j) acc[i * C::V + j] += w * v[j];
+    }
+  }
+};
+
 // A wavefront sums kC 16-byte column chunks per lane of one token, in slot order in float32, the
 // loads of B rows in flight together.  Memory-bound; with few tokens kC = 1 spreads a token's columns
 // over wavefronts.  The token's rows come from the map (an entry counts only if it points inside
@@ -1051,7 +1093,7 @@ struct Chunk<false> {
 // 64), from a look through row_pair itself, which saves the launch that fills the map.
 constexpr int kScanRows = 1024;
 
-template <bool kBF16, bool kScan, int kC, int B>
+template <bool kBF16, bool kWide, bool kScan, int kC, int B>
 __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restrict__ map,
                                                          const int32_t* __restrict__ row_pair,
                                                          const int32_t* __restrict__ fwd_off,
@@ -1105,7 +1147,7 @@ __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restri
         if (r >= 0) a = topk_w[p];
       }
       for (uint64_t m = ballot(r >= 0); m;) {   // slots in ascending order, B at a time
-        uint4 x[B][kC];
+        RowPart<kBF16, kWide> x[B][kC];
         float wt[B];
         int n = 0;
 #pragma unroll
@@ -1114,24 +1156,19 @@ __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restri
           const int jj = __builtin_ctzll(m);
           m &= m - 1;
           ++n;
-          const uint4* src = y + (int64_t)__builtin_amdgcn_readlane(r, jj) * hch;
+          const uint4* src = y + (int64_t)__builtin_amdgcn_readlane(r, jj) * hch * (kWide ? 2 : 1);
           wt[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), jj));
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             const int ch = c0 + c * kWave;
-            x[b][c] = ch < hch ? load_nt(src + ch) : make_uint4(0, 0, 0, 0);
+            x[b][c].load(src, ch, ch < hch);
           }
         }
 #pragma unroll
         for (int b = 0; b < B; ++b) {
           if (b >= n) break;
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            float v[C::V];
-            C::get(x[b][c], v);
-#pragma unroll
-            for (int q = 0; q < C::V; ++q) acc[c][q] += wt[b] * v[q];
-          }
+          for (int c = 0; c < kC; ++c) x[b][c].add(wt[b], acc[c]);
         }
       }
     }
@@ -1151,32 +1188,32 @@ __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restri
   }
 }
 
-template <bool kBF16, bool kScan, int kC, int B>
+template <bool kBF16, bool kWide, bool kScan, int kC, int B>
 void launch_tokens(const lrm_problem& p, const int32_t* map, const int32_t* row_pair,
                    const int32_t* fwd_off, const float* topk_w, const void* y, const void* residual,
                    void* out, int32_t* err, hipStream_t s) {
   const int hch = p.h * (kBF16 ? 2 : 4) / 16;
   const int64_t waves = (int64_t)p.T * ((hch + kC * kWave - 1) / (kC * kWave));
   const int64_t nb = (waves + kWavesPerBlock - 1) / kWavesPerBlock;
-  hipLaunchKernelGGL((combine_tokens<kBF16, kScan, kC, B>), dim3((unsigned)(nb < 16384 ? nb : 16384)),
+  hipLaunchKernelGGL((combine_tokens<kBF16, kWide, kScan, kC, B>), dim3((unsigned)(nb < 16384 ? nb : 16384)),
                      dim3(kBlock), 0, s, map, row_pair, fwd_off, p.E_loc, p.L_cap, p.T, p.k, topk_w,
                      (const uint4*)y, hch, (const uint4*)residual, (uint4*)out, err);
 }
 
-template <bool kBF16>
+template <bool kBF16, bool kWide>
 void launch_combine_t(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,
                       const float* topk_w, const void* y, const void* residual, void* out, char* ws,
                       hipStream_t s) {
   int32_t* err = (int32_t*)ws;
   int32_t* map = (int32_t*)(ws + kForwardMap);
   if (p.L_cap <= kScanRows && p.k <= kWave) {
-    launch_tokens<kBF16, true, 1, 8>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
+    launch_tokens<kBF16, kWide, true, 1, 8>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
     return;
   }
   const int64_t lb = ((int64_t)p.L_cap + kBlock - 1) / kBlock;
   hipLaunchKernelGGL(forward_rows, dim3((unsigned)(lb < 1 ? 1 : (lb < 2048 ? lb : 2048))), dim3(kBlock), 0, s,
                      row_pair, fwd_off, p.E_loc, p.L_cap, (int64_t)p.T * p.k, map, err);
-  launch_tokens<kBF16, false, 4, 2>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
+  launch_tokens<kBF16, kWide, false, 4, 2>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
 }
 
 }  // namespace
@@ -1190,19 +1227,22 @@ hipError_t launch_fc1_swiglu(const lrm_problem& p, const int32_t* row_pair, cons
 }
 
 hipError_t launch_fc2(const lrm_problem& p, const int32_t* fwd_off, const void* phi, const void* W,
-                      void* y, hipStream_t s) {
+                      void* y, bool wide, hipStream_t s) {
   const FcArgs g{phi, W, nullptr, fwd_off, (int64_t)p.T * p.k, p.E_loc, p.L_cap, p.k, p.d, p.h,
                  y, nullptr, nullptr, 0};
-  return p.dtype == LRM_BF16 ? launch_fc<true, false>(p, g, s) : launch_fc<false, false>(p, g, s);
+  if (p.dtype != LRM_BF16) return launch_fc<false, false>(p, g, s);
+  return wide ? launch_fc<true, false, true>(p, g, s) : launch_fc<true, false>(p, g, s);
 }
 
 hipError_t launch_combine(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,
-                          const float* topk_w, const void* y, const void* residual, void* out,
+                          const float* topk_w, const void* y, bool wide, const void* residual, void* out,
                           char* ws, hipStream_t s) {
-  if (p.dtype == LRM_BF16)
-    launch_combine_t<true>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
+  if (p.dtype != LRM_BF16)
+    launch_combine_t<false, false>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
+  else if (wide)
+    launch_combine_t<true, true>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
   else
-    launch_combine_t<false>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
+    launch_combine_t<true, false>(p, row_pair, fwd_off, topk_w, y, residual, out, ws, s);
   return hipGetLastError();
 }
 

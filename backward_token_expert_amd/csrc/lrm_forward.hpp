@@ -62,11 +62,12 @@ hipError_t launch_gate_dots(const lrm_problem& p, const int32_t* sel_pair, const
 hipError_t launch_fc1_swiglu(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,
                              const void* x, const void* W1, void* ac, void* phi, char* ws,
                              hipStream_t s);
+// wide: y in float32 for a bf16 layer too
 hipError_t launch_fc2(const lrm_problem& p, const int32_t* fwd_off, const void* phi, const void* W,
-                      void* y, hipStream_t s);
+                      void* y, bool wide, hipStream_t s);
 hipError_t launch_combine(const lrm_problem& p, const int32_t* row_pair, const int32_t* fwd_off,
-                          const float* topk_w, const void* y, const void* residual, void* out,
-                          char* ws, hipStream_t s);
+                          const float* topk_w, const void* y, bool wide, const void* residual,
+                          void* out, char* ws, hipStream_t s);
 hipError_t launch_grad_norm(const lrm_tensor* list, int32_t n, float* norm, char* ws,
                             hipStream_t s);
 hipError_t launch_clip(const lrm_tensor* list, int32_t n, float max_norm, float* norm, char* ws,

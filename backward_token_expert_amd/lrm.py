@@ -26,7 +26,8 @@ EXPORTS = ("lrm_workspace_bytes", "lrm_plan_quotas", "lrm_admit_quotas", "lrm_sc
            "lrm_status_string", "lrm_grouped_dw_dx_noalloc", "lrm_router_workspace_bytes",
            "lrm_route", "lrm_route_backward", "lrm_gate_dots", "lrm_forward_workspace_bytes",
            "lrm_grouped_fc1_swiglu", "lrm_grouped_fc2", "lrm_combine_tokens",
-           "lrm_grad_workspace_bytes", "lrm_grad_norm", "lrm_clip_grads")
+           "lrm_grad_workspace_bytes", "lrm_grad_norm", "lrm_clip_grads", "lrm_grouped_fc2_wide",
+           "lrm_combine_tokens_wide")
 _SIZES = ("lrm_workspace_bytes", "lrm_router_workspace_bytes", "lrm_forward_workspace_bytes",
           "lrm_grad_workspace_bytes")
 
@@ -127,8 +128,9 @@ def load_library(path: Optional[str] = None):
     lib.lrm_gate_dots.argtypes = [PP] + [vp] * 6 + [sz, vp]
     lib.lrm_forward_workspace_bytes.argtypes = [PP]
     lib.lrm_grouped_fc1_swiglu.argtypes = [PP] + [vp] * 7 + [sz, vp]
-    lib.lrm_grouped_fc2.argtypes = [PP] + [vp] * 5 + [sz, vp]
+    lib.lrm_grouped_fc2.argtypes = lib.lrm_grouped_fc2_wide.argtypes = [PP] + [vp] * 5 + [sz, vp]
     lib.lrm_combine_tokens.argtypes = [PP] + [vp] * 7 + [sz, vp]
+    lib.lrm_combine_tokens_wide.argtypes = [PP] + [vp] * 7 + [sz, vp]
     lib.lrm_grad_workspace_bytes.argtypes = [TP, i32]
     lib.lrm_grad_norm.argtypes = [TP, i32, vp, vp, sz, vp]
     lib.lrm_clip_grads.argtypes = [TP, i32, ctypes.c_float, vp, vp, sz, vp]
@@ -438,25 +440,33 @@ def lrm_grouped_fc1_swiglu(problem, row_pair, fwd_off, x, W1, ac, phi, ws, strea
         "lrm_grouped_fc1_swiglu")
 
 
+def _rows_of_y(p, y):
+    """y's element type and whether a bf16 layer keeps it in float32 (the calls ending in _wide)."""
+    wide = p.dtype == LRM_BF16 and getattr(y, "dtype", None) == torch.float32
+    return (_F32 if wide else _elem(p.dtype)), wide
+
+
 def lrm_grouped_fc2(problem, fwd_off, phi, W, y, ws, stream=None):
+    """``y`` in the layer's type or in float32 (lrm_grouped_fc2_wide)."""
     lib = load_library()
     p, d = problem, _device()
-    el = _elem(p.dtype)
-    _check(lib, lib.lrm_grouped_fc2(
+    el, (ty, wide) = _elem(p.dtype), _rows_of_y(p, y)
+    _check(lib, (lib.lrm_grouped_fc2_wide if wide else lib.lrm_grouped_fc2)(
         ctypes.byref(p), _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d),
         _arg(phi, "phi", el, p.L_cap * p.d, d), _arg(W, "W", el, p.E_loc * p.h * p.d, d),
-        _arg(y, "y", el, p.L_cap * p.h, d), *_space(ws, d), _queue(stream, d)), "lrm_grouped_fc2")
+        _arg(y, "y", ty, p.L_cap * p.h, d), *_space(ws, d), _queue(stream, d)), "lrm_grouped_fc2")
 
 
 def lrm_combine_tokens(problem, row_pair, fwd_off, topk_w, y, residual, out, ws, stream=None):
-    """``residual`` None: the experts' output alone; ``out`` may be ``residual``."""
+    """``residual`` None: the experts' output alone; ``out`` may be ``residual``; ``y`` in the layer's
+    type or in float32 (lrm_combine_tokens_wide)."""
     lib = load_library()
     p, d = problem, _device()
-    el = _elem(p.dtype)
-    _check(lib, lib.lrm_combine_tokens(
+    el, (ty, wide) = _elem(p.dtype), _rows_of_y(p, y)
+    _check(lib, (lib.lrm_combine_tokens_wide if wide else lib.lrm_combine_tokens)(
         ctypes.byref(p), _arg(row_pair, "row_pair", _I32, p.L_cap, d),
         _arg(fwd_off, "fwd_off", _I32, p.E_loc + 1, d), _arg(topk_w, "topk_w", _F32, p.T * p.k, d),
-        _arg(y, "y", el, p.L_cap * p.h, d), _arg(residual, "residual", el, p.T * p.h, d),
+        _arg(y, "y", ty, p.L_cap * p.h, d), _arg(residual, "residual", el, p.T * p.h, d),
         _arg(out, "out", el, p.T * p.h, d), *_space(ws, d), _queue(stream, d)), "lrm_combine_tokens")
 
 

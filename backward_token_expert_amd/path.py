@@ -175,14 +175,15 @@ def route(router, logits, rb: RouterBuffers, mask=None, stream=None):
 
 class ForwardBuffers:
     """Outputs of the experts' forward, sized to the problem's capacities.  ``keep_ac`` False (serving):
-    FC1's output is not kept for a backward."""
+    FC1's output is not kept for a backward.  ``wide_y``: a bf16 layer's expert outputs are kept in
+    float32 on their way to the tokens, so that out is rounded once (see lrm_combine_tokens_wide)."""
 
-    def __init__(self, problem: lrm.Problem, device="cuda", keep_ac: bool = True):
+    def __init__(self, problem: lrm.Problem, device="cuda", keep_ac: bool = True, wide_y: bool = False):
         p = problem
         st = storage_dtype("bf16" if p.dtype == lrm.LRM_BF16 else "f32")
         self.ac = torch.zeros((p.L_cap, 2 * p.d), dtype=st, device=device) if keep_ac else None
         self.phi = torch.zeros((p.L_cap, p.d), dtype=st, device=device)
-        self.y = torch.zeros((p.L_cap, p.h), dtype=st, device=device)
+        self.y = torch.zeros((p.L_cap, p.h), dtype=torch.float32 if wide_y else st, device=device)
         self.out = torch.zeros((p.T, p.h), dtype=st, device=device)
 
 

@@ -471,8 +471,8 @@ lrm_status lrm_scatter_tokens(const lrm_problem* problem, const int32_t* sel_pai
  *  - Router calls have a problem of their own (lrm_router) and a workspace of
  *    lrm_router_workspace_bytes; its first word is the error word, which lrm_route sets to the
  *    bits of that call.
- *  - lrm_grouped_fc1_swiglu, lrm_grouped_fc2, lrm_combine_tokens and lrm_gate_dots need a workspace of
- *    lrm_forward_workspace_bytes only (lrm_workspace_bytes of the same problem is always
+ *  - lrm_grouped_fc1_swiglu, lrm_grouped_fc2, lrm_combine_tokens (also their _wide forms) and
+ *    lrm_gate_dots need a workspace of lrm_forward_workspace_bytes only (lrm_workspace_bytes of the same problem is always
  *    enough, so a training step may pass the one it has).  They may overwrite all of those bytes
  *    but the error word, so not between lrm_score_norms and lrm_score_combine on one workspace.
  *  - In those four calls L_cap and K_cap may be 0 (a share without a row); the arrays of rows, which
@@ -591,6 +591,11 @@ lrm_status lrm_grouped_fc1_swiglu(const lrm_problem* problem, const int32_t* row
 lrm_status lrm_grouped_fc2(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
                            const void* W, void* y, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* The same with y float32 [L_cap][h], unrounded, whatever the layer's type. */
+lrm_status lrm_grouped_fc2_wide(const lrm_problem* problem, const int32_t* fwd_off, const void* phi,
+                                const void* W, float* y, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
 /*
  * The experts' output rows back to their tokens, weighted, with the residual:
  *   out[t] = RNE_dtype( residual[t] + sum over slots j = 0..k-1 in order, pair p = t*k + j with a
@@ -607,6 +612,16 @@ lrm_status lrm_combine_tokens(const lrm_problem* problem, const int32_t* row_pai
                               const int32_t* fwd_off, const float* topk_w, const void* y,
                               const void* residual, void* out, void* ws, size_t ws_bytes,
                               hipStream_t stream);
+
+/*
+ * The same with y float32 [L_cap][h] (lrm_grouped_fc2_wide's).  In a bf16 layer y's own rounding
+ * (2^-8 |y| at most) reaches out as sum_p topk_w[p] 2^-8 |y|, which exceeds out's rounding where a
+ * token's terms cancel; with float32 rows out carries its own rounding alone, for twice y's bytes.
+ */
+lrm_status lrm_combine_tokens_wide(const lrm_problem* problem, const int32_t* row_pair,
+                                   const int32_t* fwd_off, const float* topk_w, const float* y,
+                                   const void* residual, void* out, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
 
 /*
  * Global norm of many tensors, and clipping.  The list is host memory, read during the call only.
