@@ -202,11 +202,15 @@ def run_forward(problem, policy, topk_idx, topk_w, x, W1, W, bufs: DeviceBuffers
 
 
 def run_router_backward(problem, router, logits, bufs: DeviceBuffers, rb: RouterBuffers,
-                        stream=None):
+                        stream=None, balance: bool = True):
     """Enqueue the router's gradient after ``run`` on the same buffers: rb.dlogits holds that of the
-    balance loss and of the retained pairs' gate weights."""
+    balance loss and of the retained pairs' gate weights.  Where a layer's experts are shared out and
+    the shares' dlogits are summed, ``balance`` is True on one share alone: each holds the gate terms
+    of its own pairs, but the balance loss of the whole layer."""
     lrm.lrm_gate_dots(problem, bufs.sel_pair, bufs.cmp_off, bufs.dphi, bufs.Phic, rb.adot, bufs.ws,
                       stream)
+    if not balance:
+        router = lrm.make_router(router.T, router.E, router.k, router.dtype, router.gate, 0.0)
     lrm.lrm_route_backward(router, logits, rb.topk_idx, rb.topk_w, rb.counts, rb.adot,
                            rb.dlogits, stream)
 

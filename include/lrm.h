@@ -552,6 +552,9 @@ lrm_status lrm_gate_dots(const lrm_problem* problem, const int32_t* sel_pair,
  * lowest value no longer holds the logarithm.  Rows of tokens that lrm_route found not valid (topk_idx[t*k] < 0) are zeros.
  *  in : logits [T][E]; topk_idx, topk_w, counts as lrm_route wrote them; adot float32 [T*k] or NULL
  *  out: dlogits float32 [T][E] (every row written)
+ * Shares of a layer: adot holds a share's own pairs, and the gate's terms are linear in it, so the
+ * dlogits of all shares sum to the layer's; the balance term is whole in every call.  Where dlogits
+ * are summed over shares, all calls but one take a router with balance_coef = 0.
  * Needs no workspace.  logits and dlogits must be 16-byte aligned; chosen experts outside [0, E)
  * are skipped.
  */
