@@ -1089,9 +1089,13 @@ struct RowPart {
 // A wavefront sums kC 16-byte column chunks per lane of one token, in slot order in float32, the
 // loads of B rows in flight together.  Memory-bound; with few tokens kC = 1 spreads a token's columns
 // over wavefronts.  The token's rows come from the map (an entry counts only if it points inside
-// [0, L) at a row that names the pair, so stale entries are ignored), or, with kScan (few rows, k <=
-// 64), from a look through row_pair itself, which saves the launch that fills the map.
-constexpr int kScanRows = 1024;
+// [0, L) at a row that names the pair, so stale entries are ignored), or, with kScan (k <= 64), from a
+// look through row_pair itself, which saves the launch that fills the map.  Every wavefront then reads
+// all row ids, so that is for few of both; scan / map in us for 2048 columns in bf16:
+//   256 rows,    32 tokens (128 wavefronts)  4.0 / 6.8     1024 rows, 128 tokens (512)    6.0 / 7.6
+//   1024 rows,  512 tokens (2048)            5.5 / 5.8     1024 rows, 1024 tokens (4096)  6.7 / 5.7
+//   1024 rows, 8192 tokens (32768)          31.8 / 13.3    1024 rows, 32768 tokens       89.4 / 26.5
+constexpr int kScanRows = 1024, kScanWaves = 2048;
 
 template <bool kBF16, bool kWide, bool kScan, int kC, int B>
 __global__ __launch_bounds__(kBlock) void combine_tokens(const int32_t* __restrict__ map,
@@ -1206,7 +1210,8 @@ void launch_combine_t(const lrm_problem& p, const int32_t* row_pair, const int32
                       hipStream_t s) {
   int32_t* err = (int32_t*)ws;
   int32_t* map = (int32_t*)(ws + kForwardMap);
-  if (p.L_cap <= kScanRows && p.k <= kWave) {
+  const int64_t waves = (int64_t)p.T * ((p.h * (kBF16 ? 2 : 4) / 16 + kWave - 1) / kWave);
+  if (p.L_cap <= kScanRows && waves <= kScanWaves && p.k <= kWave) {
     launch_tokens<kBF16, kWide, true, 1, 8>(p, map, row_pair, fwd_off, topk_w, y, residual, out, err, s);
     return;
   }
