@@ -268,8 +268,9 @@ __device__ __forceinline__ void merge_lanes(double (&t)[KT]) {
   }
 }
 
-// exp(v - m) for v <= m by the hardware's power of two.  The argument's two roundings put it off by at
-// most 2 (m - v) 2^-24 of itself, and so by less than 2^-24 of the row's largest.
+// exp(v - m) for v <= m by the hardware's power of two.  The argument's two roundings and the constant's
+// put it off by at most 2.3 (m - v) 2^-24 of itself, the instruction by 2 2^-24 more: in all less than 3
+// 2^-24 of the row's largest, which is what the sum and the weights' sum to 1 rest on.
 __device__ __forceinline__ float exp_below(float v, float m) {
   return __builtin_amdgcn_exp2f((v - m) * 1.44269504f);
 }
@@ -780,12 +781,16 @@ unsigned launch_rows(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
   return nb;
 }
 
-constexpr int kShortBatch = 4096;   // tokens
+// Up to this many tokens (one pass of 256 workgroups) the shapes with more lanes a token.  Router /
+// gradient in us, E 128, k 8, f32, with 16 lanes against 8: 256 tokens 10.0 / 4.6 against 14.0 / 6.8; 4096
+// 11.4 / 4.8 against 14.8 / 7.1; 8192 12.5 / 5.6 against 15.1 / 7.4; 16384 15.2 / 7.4 against 15.9 / 8.6, with
+// bf16 logits 14.8 / 8.9 against 15.1 / 8.2; 32768 21.9 / 15.9 against 19.4 / 14.0.
+constexpr int kShortBatch = 8192;
 
 template <bool kBF16, int KT>
 unsigned launch_rows_e(const RouteArgs& a, const RouteOut& o, hipStream_t s) {
   // few tokens: more lanes each, for the latency of one token's chain (one token 10.4 us with 4
-  // lanes, 7.2 with 8, 5.8 with 16); 32768 tokens take 19.4 us with 8 and 21.9 with 16
+  // lanes, 7.2 with 8, 5.8 with 16)
   if (a.E <= 128 && a.T <= kShortBatch) return launch_rows<kBF16, 16, 8, KT, 8>(a, o, s);
   if (a.E <= 128) return launch_rows<kBF16, 8, 16, KT, 16>(a, o, s);
   if (a.E <= 256) return launch_rows<kBF16, 8, 32, KT, 8>(a, o, s);
@@ -821,7 +826,7 @@ template <bool kBF16>
 void launch_back_e(const lrm_router& r, const void* logits, const int32_t* topk_idx,
                    const float* topk_w, const int32_t* counts, const float* adot, float* dlogits,
                    hipStream_t s) {
-  // 32768 tokens: 19.2 us with 4 lanes a token, 14.0 with 8, 15.9 with 16; 1021: 6.6, 4.8 and 4.2
+  // 32768 tokens: 19.2 us with 4 lanes a token; 1021: 6.6 with 4, 4.8 with 8, 4.2 with 16
   if (r.E <= 128 && r.T <= kShortBatch)
     return launch_back<kBF16, 16, 8, 4>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
   if (r.E <= 128) return launch_back<kBF16, 8, 16, 4>(r, logits, topk_idx, topk_w, counts, adot, dlogits, s);
