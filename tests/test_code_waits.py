@@ -107,8 +107,9 @@ def dpp_rule(ins):
 RULES = {"m0": m0_rule, "scalar": scalar_rule, "dpp": dpp_rule}
 
 
-def broken(text, rule):
-    pairs = [(RULES[rule](ins), ins) for code in functions(text) for ins in code]
+def broken(code, rule):
+    """The pairs of instructions in a list of functions that `rule` finds too near."""
+    pairs = [(RULES[rule](ins), ins) for function in code for ins in function]
     return [(near.text, ins.text) for near, ins in pairs if near]
 
 
@@ -127,7 +128,8 @@ RIGHT = [("scalar", "v_readfirstlane_b32 s4, v0\n s_nop 4\n buffer_load_dwordx4 
 
 
 def listing(code):
-    return "<f>:\n" + "\n".join("\t%s    // %012X: 00" % (c.strip(), 4 * i) for i, c in enumerate(code.split("\n")))
+    return functions("<f>:\n" + "\n".join("\t%s    // %012X: 00" % (c.strip(), 4 * i)
+                                          for i, c in enumerate(code.split("\n"))))
 
 
 def test_the_check_itself():
@@ -137,16 +139,16 @@ def test_the_check_itself():
     loop = ("<f>:\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds    // 000000000000: 00\n"
             "\ts_mov_b32 m0, s9    // 000000000008: 00\n"
             "\ts_branch 65532    // 00000000000C: BF82FFFC\n")
-    assert not broken(loop, "m0")            # the branch itself is a wait state
+    assert not broken(functions(loop), "m0")            # the branch itself is a wait state
     dpp = ("<f>:\n\tv_mov_b32_dpp v9, v3 quad_perm:[1,0,3,2]    // 000000000000: 00\n"
            "\tv_max_f64 v[2:3], v[4:5], v[6:7]    // 000000000008: 00\n"
            "\ts_cbranch_scc1 65532    // 00000000000C: BF85FFFC\n")
-    assert len(broken(dpp, "dpp")) == 1
+    assert len(broken(functions(dpp), "dpp")) == 1
 
 
 @pytest.fixture(scope="module")
 def code(tmp_path_factory):
-    """The disassemblies of the library's device code."""
+    """The functions of the library's device code."""
     if not os.path.exists(OBJDUMP):
         pytest.skip("no llvm-objdump")
     where = tmp_path_factory.mktemp("code")
@@ -154,12 +156,12 @@ def code(tmp_path_factory):
     subprocess.run([OBJDUMP, "--offloading", "liblrm.so"], check=True, stdout=subprocess.DEVNULL, cwd=where)
     objects = sorted(f for f in os.listdir(where) if "amdgcn" in f)
     assert objects
-    return [subprocess.run([OBJDUMP, "-d", "--no-leading-addr", f], check=True, cwd=where,
-                           capture_output=True, text=True).stdout for f in objects]
+    return [f for o in objects for f in functions(subprocess.run(
+        [OBJDUMP, "-d", "--no-leading-addr", o], check=True, cwd=where, capture_output=True, text=True).stdout)]
 
 
 @pytest.mark.parametrize("rule", sorted(RULES))
 def test_compiled_kernels_keep_the_wait_states(code, rule):
-    assert sum(t.count(" lds ") for t in code) > 1000      # the listings hold the loads
-    found = [pair for text in code for pair in broken(text, rule)]
+    assert sum("lds" in ins.args for function in code for ins in function) > 1000   # the loads are there
+    found = broken(code, rule)
     assert not found, f"{len(found)} of too few wait states, the first: {found[:4]}"
