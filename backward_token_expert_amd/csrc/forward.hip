@@ -971,11 +971,28 @@ using MidFew = Shape<4, 2, 2, 2, 3, true>;   // 128 x 256
 using Mid = Shape<4, 2, 2, 2, 3>;
 using Big = Shape<4, 2, 2, 4, 2>;            // 256 x 256
 constexpr int kMidRows = 24, kSpreadRows = 96, kBigRows = 256;
-// Tokens up to which fc_few is the faster one: bf16 FC1 / FC2 of one token 18.3 / 8.9 against Low's
-// 21.4 / 11.9 (h 4096, d 1408: 40.7 / 22.5, 39.5 / 19.1), of two there 52.3 / 28.5 against 42.3 / 25.8;
-// float32 (h = d = 512, 32 experts) 27 / 19 against fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at
-// 256.
-constexpr int kFewBF16 = 1, kFewF32 = 128;
+// fc_few's share.  bf16: one token, while its experts make at most kFewUnits units of Low, half a unit a
+// CU; us of FC1 / FC2 with fc_few against Low, of 8 experts in turn through 128:
+//   h 1024, d 512    8.4 /  5.8 (64 and 64 units)    12.7 /  8.9
+//   h 2048, d 768   17.4 /  9.1 (96, 128)            20.2 / 11.0
+//   h 2048, d 1024  21.2 / 11.1 (128, 128)           20.4 / 12.7
+//   h 4096, d 768   28.1 / 14.0 (96, 256)            34.8 / 12.9
+//   h 4096, d 1024  30.8 / 18.7 (128, 256)           35.4 / 14.9
+//   h 2560, d 1536  29.6 / 17.8 (192, 160)           27.4 / 17.3
+//   h 4096, d 1408  39.9 / 21.8 (176, 256)           37.1 / 18.9
+// and two tokens there 52.3 / 28.5 against 42.3 / 25.8.  float32 (h = d = 512, 32 experts) 27 / 19 against
+// fc_f32's 44 / 32 at 64 tokens, 57 / 31 against 46 / 44 at 256.
+constexpr int kFewBF16 = 1, kFewUnits = 128, kFewF32 = 128;
+
+// The product has few enough rows and columns for fc_few; N its columns (of one half).
+template <bool kBF16, bool kSwiglu>
+bool takes_few(const lrm_problem& p, int N) {
+  if (p.T > (kBF16 ? kFewBF16 : kFewF32)) return false;
+  if (!kBF16) return true;
+  const int bn = kSwiglu ? Low::BW / 2 : Low::BW;
+  const int64_t local = (int64_t)p.T * p.k * p.E_loc / p.E;   // rows, and so experts, of a balanced load
+  return (local > 1 ? local : 1) * ((N + bn - 1) / bn) <= kFewUnits;
+}
 
 template <class C, bool kSwiglu, bool kWide>
 hipError_t launch_shape(const FcArgs& g, hipStream_t s) {
@@ -988,7 +1005,7 @@ hipError_t launch_shape(const FcArgs& g, hipStream_t s) {
 template <bool kBF16, bool kSwiglu, bool kWide = false>
 hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
   if (p.L_cap == 0) return hipSuccess;   // no row
-  if (p.T <= (kBF16 ? kFewBF16 : kFewF32)) {   // an expert is chosen once a token: T rows at most
+  if (takes_few<kBF16, kSwiglu>(p, g.N)) {   // an expert is chosen once a token: T rows at most
     if constexpr (kBF16) {
       launch_few<kBF16, kSwiglu, kWide, 1>(p, g, s);
     } else {

@@ -162,3 +162,15 @@ def test_wild_offsets_stay_inside_the_buffers(T, dtype):
     lrm.lrm_combine_tokens(c.P, rp, off, _dev(c.w), y, None, ob[300:300 + c.T], c.ws)
     assert lrm.lrm_read_device_error(c.ws, clear=True) == 32
     assert bool((ob[:300] == 5.0).all()) and bool((ob[300 + c.T:] == 5.0).all())
+
+
+@pytest.mark.parametrize("h,d", [(1032, 4104), (4104, 1032), (2048, 1024)])
+def test_one_token_of_wide_and_narrow_products(h, d):
+    """One token's products on either side of what the serving kernel takes (by its units of work)."""
+    c = Case(T=1, k=8, E=8, e_lo=0, E_loc=8, h=h, d=d, dtype="bf16")
+    check_fc1(c)
+    check_fc1(c, keep_ac=False)
+    check_fc2(c, residual=True)
+    s = Case(T=1, k=8, E=32, e_lo=8, E_loc=8, h=h, d=d, dtype="bf16")     # a share: two of its experts
+    check_fc1(s)
+    check_fc2(s, residual=False)
