@@ -71,8 +71,10 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ fwd_off
 
 __device__ __forceinline__ float silu_mul(float a, float c) { return a / (1.0f + expf(-a)) * c; }
 
-// The same with the hardware's power of two and reciprocal (each off by about 2^-23), for outputs that
-// are rounded to bf16: the exact forms took 7 % of FC1's time.  exp(-a) = infinity gives 0, as it should.
+// The same with the hardware's power of two and reciprocal, for outputs that are rounded to bf16: the
+// exact forms took 7 % of FC1's time.  Each is off by about 2^-23 of itself, the power by |a| 2^-23 more
+// from its rounded argument (2^-16.5 at the largest a it tells from infinity, against the 2^-8 of bf16).
+// exp(-a) = infinity gives 0, as it should.
 __device__ __forceinline__ float silu_mul_fast(float a, float c) {
   return a * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.44269504f)) * c;
 }
@@ -114,8 +116,8 @@ constexpr uint32_t kOutOfRange = 0x80000000u;
 // turn, cyclically.  Units that all start at 0 read the same few hundred bytes of every weight row at
 // a time, and where the rows' pitch is a power of two those lie in a few of the memory's channels:
 // FC1 of 32 tokens (h 2048, d 768, 150 MB of weights in use) took 45.0 us so and takes 37.5 (34.0 with
-// the weights past the caches).  A row's sum depends on its expert and column alone, not on the batch
-// around it.
+// the weights past the caches).  A row's sum depends on its expert and column alone among the rows of a
+// problem; the tile shape, and with it the order, follows from the problem's sizes and capacity.
 __device__ __forceinline__ int first_step(int c, int e, int n) {
   return (int)((5u * (unsigned)c + 7u * (unsigned)e) % (unsigned)n);
 }
@@ -134,14 +136,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand(const char* base) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// float32 products: 64 rows x 64 columns (for kSwiglu 32 of each half) by 2 wavefronts, each one 32
-// rows x two 32-wide column tiles, which for kSwiglu are the same columns of the gate and the up
-// half.  Bound by the float32 matrix rate (64 cycles an MFMA, against one 16-byte LDS read a lane
-// for four of them): the next K step's loads are in registers while one is multiplied, and a CU's
-// many small workgroups cover each other's barriers.  A lane's 16 bytes hold four k of one row; the i-th
-// MFMA takes the i-th of both operands, so k = 8 s + i and 8 s + 4 + i meet, in any order.
-// kLong: runs of 128 k are summed apart and then added, so that a long row's sum is no less exact
-// than a short one's; without the second set of accumulators 12 workgroups fit a CU, not 8.
+// float32 products: 64 rows x 128 weight rows (for kSwiglu 64 of each half, so 64 output columns) by 4
+// wavefronts, each one 32 rows x two 32-wide column tiles, which for kSwiglu are the same columns of the
+// gate and the up half.  Bound by the float32 matrix rate (64 cycles an MFMA, against three 16-byte LDS
+// reads a lane for eight of them): the next K step's loads are in registers while one is multiplied, and
+// a CU's many small workgroups cover each other's barriers.  A lane's 16 bytes hold four k of one row;
+// the i-th MFMA takes the i-th of both operands, so k = 8 s + i and 8 s + 4 + i meet, in any order.
+// kLong: runs of 128 k are summed apart and then added, so that a long row's sum is no less exact than
+// a short one's; that second set of accumulators takes 124 registers a lane and leaves 4 workgroups a
+// CU, without it 80 leave 6.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBM = 64, kBNH = 64, kKS = 16, kPitch = kKS + 4, kRun = 128, kLongK = 512, kF32Threads = 256;
 
@@ -291,8 +294,11 @@ struct Shape {
   static constexpr int T_BYTES = BT * ROW, W_BYTES = BW * ROW, STG = T_BYTES + W_BYTES;
   static constexpr int IT = T_BYTES / 1024 / NW, IW = W_BYTES / 1024 / NW, I = IT + IW;
   static_assert(IT * 1024 * NW == T_BYTES && IW * 1024 * NW == W_BYTES, "whole 1 KiB blocks a wave");
-  // For few rows an expert: units start at K steps of their own (see first_step), and the weights,
-  // of which a workgroup then reads every line alone, pass the caches by.
+  // For few rows an expert: units start at K steps of their own (see first_step), and the weights pass
+  // the caches by: with one row tile an expert a workgroup reads every line of them alone.  A hot
+  // expert's further row tiles read them from memory again, and a small layer's weights, which could
+  // stay in the memory-side cache between calls, do not (two tokens, three sets of weights in turn:
+  // 23.8 us against 19.5; twelve sets, as in a model: 22.9 against 24.8).
   static constexpr bool SPREAD = kSpread_;
   static constexpr int TABLE = 1024 + 1;                  // tiles before each expert
   // FC2's outputs go through 2 KiB of LDS a wavefront where as many workgroups still fit a CU.
@@ -1020,7 +1026,8 @@ hipError_t launch_fc(const lrm_problem& p, FcArgs g, hipStream_t s) {
   }
   if constexpr (kBF16) {
     // rows of an expert: the capacity's share, unless that is far above the balanced load T k / E (a
-    // share of a layer has capacity for every pair)
+    // share of a layer has capacity for every pair).  Four times that load is for skewed routing; where a
+    // share's is balanced, the shape is one for more rows than there are (the table: up to 13 % slower)
     const int64_t cap = (int64_t)p.L_cap / p.E_loc, most = 4 * ((int64_t)p.T * p.k / p.E);
     const int64_t rows = cap < most ? cap : most;
     if (rows >= kBigRows) return launch_shape<Big, kSwiglu, kWide>(g, s);

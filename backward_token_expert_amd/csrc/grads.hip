@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kInFlight = 8;                           // 16-byte accesses of a thread at a time
-constexpr int64_t kKeepBytes = (int64_t)192 << 20;      // of the list's end, for the second pass
+constexpr int64_t kKeepBytes = (int64_t)192 << 20;      // of a launch's end, for the second pass
 constexpr int kChunkBytes = kBlock * kInFlight * 16;
 __host__ __device__ constexpr int chunk_elems(bool bf16) { return kChunkBytes / (bf16 ? 2 : 4); }
 
@@ -70,7 +70,8 @@ __device__ __forceinline__ double add_squares(double acc, uint4 q) {
 }
 
 // Elements [i0, i1) of src, i0 a multiple of the chunk: this thread's sum of squares.  `keep`: the
-// clipping reads them again soon; otherwise they pass the caches by.
+// clipping reads them again soon; otherwise they pass the caches by.  (Up to kTensorsPerLaunch tensors
+// the launch's end is the list's; of a longer list each launch keeps its own.)
 template <bool kBF16>
 __device__ __forceinline__ double chunk_squares(const void* src, int64_t i0, int64_t i1, bool keep) {
   constexpr int V = kBF16 ? 8 : 4;
@@ -191,9 +192,10 @@ __device__ __forceinline__ void chunk_scale(const void* src, void* dst, int64_t 
   }
 }
 
-// Every workgroup forms the norm from the partial sums itself (a few KB from L2), which saves a
-// launch between the two passes.  The chunks are taken from the last to the first: what the norm's
-// pass read last is still in the memory-side cache (256 MB).
+// Every workgroup forms the norm from the partial sums itself, which saves a launch between the two
+// passes: 8 KB from L2 for one launch of 1024 workgroups, as much again for every further one.  The
+// chunks are taken from the last to the first: what the norm's pass read last is still in the
+// memory-side cache (256 MB).
 __global__ __launch_bounds__(kBlock) void grad_scale(GradList l, const double* __restrict__ part,
                                                      int64_t parts, float max_norm,
                                                      float* __restrict__ norm,

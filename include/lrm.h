@@ -472,10 +472,11 @@ lrm_status lrm_scatter_tokens(const lrm_problem* problem, const int32_t* sel_pai
  *    lrm_router_workspace_bytes; its first word is the error word, which lrm_route sets to the
  *    bits of that call.
  *  - lrm_grouped_fc1_swiglu, lrm_grouped_fc2, lrm_combine_tokens (also their _wide forms) and
- *    lrm_gate_dots need a workspace of lrm_forward_workspace_bytes only (lrm_workspace_bytes of the same problem is always
- *    enough, so a training step may pass the one it has).  They may overwrite all of those bytes
- *    but the error word, so not between lrm_score_norms and lrm_score_combine on one workspace.
- *  - In those four calls L_cap and K_cap may be 0 (a share without a row); the arrays of rows, which
+ *    lrm_gate_dots need a workspace of lrm_forward_workspace_bytes only (lrm_workspace_bytes of the
+ *    same problem is always enough, so a training step may pass the one it has).  They may overwrite
+ *    all of those bytes but the error word, so not between lrm_score_norms and lrm_score_combine on
+ *    one workspace.
+ *  - In those calls L_cap and K_cap may be 0 (a share without a row); the arrays of rows, which
  *    are empty then, may be NULL.
  *  - Two calls that may run at the same time need a workspace each.
  * ------------------------------------------------------------------------------------------------ */
@@ -501,7 +502,8 @@ size_t lrm_router_workspace_bytes(const lrm_router* router);
  * auxiliary loss: L_aux = coef * E * sum_e f_e P_e).  For every token t with mask[t] != 0:
  *   lse[t]   = log sum_e exp(l_te),   p_te = exp(l_te - lse[t])
  *   the k chosen experts in the order (logit descending, expert ascending), and their weights
- *   under `gate`, each rounded once to float32 from float32 arithmetic;
+ *   under `gate`, in float32 arithmetic (an exponential of l - max is off by at most
+ *   (2.3 |l - max| + 2) 2^-24 of itself);
  * and over the n valid tokens
  *   counts[e] = pairs of expert e,  prob[e] = P_e = (1/n) sum_t p_te,
  *   loss = balance_coef * E * sum_e f_e P_e  with  f_e = counts[e] / (n k)
